@@ -32,6 +32,13 @@
  *                                   the layer from hidden states + router gate
  *   mx_dequantize_bf16_2d           load-time dequant of an MXFP8 router gate
  *
+ * and what stands around it in a transformer block:
+ *   mx_add_rmsnorm_quant            residual addition + RMS norm, MXFP8 rows out
+ *   mxfp8_linear_fused              MXFP8 product with bias, activation and
+ *                                   residual in its epilogue, bf16 or MXFP8 out
+ *   moe_balance_loss                the router's load-balance loss, per-expert
+ *                                   counts and the gradient of the logits
+ *
  * Formats.  An MX block is 32 consecutive elements along the contraction
  * axis K.  Payload: one float8_e4m3fn byte per element.  Scale: one UE8M0
  * (e8m0) byte per block, value 2^(byte - 127), chosen as
@@ -372,6 +379,97 @@ mxmoe_status mxfp4_linear(const uint16_t* x, const uint8_t* wp, const uint8_t* w
 mxmoe_status mxfp4_linear_mma_scales(const uint16_t* x, const uint8_t* wp, const uint8_t* ws_mma,
                                      int64_t M, int64_t N, int64_t K, uint16_t* out,
                                      void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Residual addition, root-mean-square norm and MXFP8 quantization of the rows
+ * the next product reads:
+ *
+ *   h = x + residual     fp32, rounded to the residual's type (h = x without one)
+ *   y = bf16( h * w / sqrt(mean(h^2) + eps) )     mean over the H elements, fp32
+ *   q, scale = MX-quant(y), the bytes of mx_quantize_3d on y
+ *
+ *   x             bf16 [M, H], rows ldx elements apart (ldx >= H, ldx % 8 == 0),
+ *                 16-byte aligned
+ *   residual      NULL, or [M, H] contiguous, bf16 or (residual_fp32 != 0) fp32
+ *   residual_out  h in the residual's type; may be `residual` itself; NULL
+ *                 exactly when residual is
+ *   weight        [H] bf16 or (weight_fp32 != 0) fp32
+ *   y             bf16 [M, H] (NULL: not written), e.g. for the router gate
+ *   q             e4m3 [M, H]
+ *   scale         e8m0 [M, ceil(H/32)], or (mma_layout != 0) the MMA layout:
+ *                 ceil(M/128) * ceil(H/128) * 512 bytes, rows past M unwritten
+ * residual, residual_out, weight and y are 32-byte aligned, q and scale
+ * 16-byte.  Requires H % 16 == 0, 16 <= H <= 32768, eps >= 0.  M == 0 is a no-op.
+ * A row whose squares overflow fp32 (|h| above about 1e19) gives y = 0.
+ */
+mxmoe_status mx_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* residual,
+                                  int residual_fp32, void* residual_out, const void* weight,
+                                  int weight_fp32, float eps, int64_t M, int64_t H, uint16_t* y,
+                                  uint8_t* q, uint8_t* scale, int mma_layout, void* stream);
+
+/*
+ * Dense MXFP8 product with bias, activation and residual in its epilogue:
+ *
+ *   z[m, n] = sum_k deq(xq)[m, k] * deq(wq)[n, k] + bias[n]      fp32
+ *   v       = act(z)
+ *   out     = bf16(v + residual), rounded once;  or
+ *   out_q, out_s = MX-quant(v) along N (v in fp32), what the next product reads
+ *
+ *   x          bf16 [M, K], MX-quantized into the workspace (the rule of
+ *              mx_quantize_3d); or NULL, and then
+ *   xq, xs     e4m3 [M, K] and its scales in the MMA layout (mx_add_rmsnorm_quant
+ *              with mma_layout, or out_q / out_s of another call)
+ *   wq, ws     e4m3 [N, K] and its scales in the MMA layout
+ *              (mx_scales_to_mma_layout(ws, 1, N, K))
+ *   bias       NULL, or [N] bf16 / (bias_fp32 != 0) fp32
+ *   act        0 none, 1 relu, 2 gelu (erf), 3 gelu (tanh form), 4 silu
+ *   residual   NULL, or bf16 [M, N] (with out only); may be `out` itself
+ *   out        bf16 [M, N], or NULL, and then
+ *   out_q      e4m3 [M, N]
+ *   out_s      its scales in the MMA layout, ceil(M/128) * ceil(N/128) * 512
+ *              bytes, rows past M unwritten
+ *   workspace  mxfp8_linear_fused_workspace_size(M, K) bytes, 256-byte aligned,
+ *              when x is given; unused otherwise
+ * All pointers 16-byte aligned.  Requires K % 16 == 0, N % 16 == 0, M < 2^24.
+ * M == 0 is a no-op.
+ */
+size_t mxfp8_linear_fused_workspace_size(int64_t M, int64_t K);
+mxmoe_status mxfp8_linear_fused(const uint16_t* x, const uint8_t* xq, const uint8_t* xs,
+                                const uint8_t* wq, const uint8_t* ws, int64_t M, int64_t N,
+                                int64_t K, const void* bias, int bias_fp32, int act,
+                                const uint16_t* residual, uint16_t* out, uint8_t* out_q,
+                                uint8_t* out_s, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The router's load-balance loss, the per-expert counts and the gradient of
+ * the logits:
+ *
+ *   p_te = softmax(logits[t, :])_e        n = tokens with mask[t] != 0
+ *   counts[e] = assignments of those tokens to expert e
+ *   f_e  = c_e / sum_e c_e, c = counts_in when given (e.g. counts summed over
+ *          micro-batches or ranks), counts otherwise
+ *   loss = coef * E * sum_e f_e * (1/n) sum_t p_te          over those tokens
+ *   dlogits[t, e] = coef * E / n * p_te * (f_e - sum_j p_tj f_j); 0 where masked
+ *
+ *   logits     fp32 [T, E], rows ldl elements apart (ldl >= E)
+ *   topk_ids   int32 [T, k]; ids of masked tokens are not read; an id outside
+ *              [0, E) records MXMOE_ERR_DEVICE_CHECK and is not counted
+ *   mask       NULL (every token counts) or uint8 [T]
+ *   counts_in  NULL or int64 [E], non-negative
+ *   loss       fp32 [1];  counts int64 [E]
+ *   dlogits    fp32 [T, E] contiguous; NULL: no gradient
+ *   ws         moe_balance_loss_workspace_size(T, E) bytes, 16-byte aligned
+ * With n = 0 or no assignment, loss and gradient are 0.  A logit of -inf has
+ * probability 0, also in a row of nothing else; a masked token's logits are not
+ * read.  Sums run in a fixed order: the same inputs give the same bits.
+ * Requires 1 <= E <= 1024, 1 <= k <= min(E, 32), T * k < 2^31.  Pointers are
+ * aligned to their elements.
+ */
+size_t moe_balance_loss_workspace_size(int64_t T, int E);
+mxmoe_status moe_balance_loss(const float* logits, int64_t ldl, const int32_t* topk_ids,
+                              const uint8_t* mask, const int64_t* counts_in, int64_t T, int E,
+                              int k, float coef, float* loss, int64_t* counts, float* dlogits,
+                              void* ws, size_t ws_bytes, void* stream);
 
 /*
  * moe_forward_mxfp8 with the weight scales already in the MMA layout

@@ -2,8 +2,10 @@
 
 The compute path is the C-ABI library ``libmxmoe.so`` (hand-written CUDA,
 tcgen05 tensor cores), with W4A8 (MXFP4 expert weights) and W4A4 (MXFP4
-weights and expert inputs) variants and the dense MXFP8 / W4A4 linear (one
-group of the grouped GEMM); ``api`` is
+weights and expert inputs) variants, the dense MXFP8 / W4A4 linear (one
+group of the grouped GEMM) and the operators around the expert forward in a
+transformer block (RMS norm with MXFP8 output, fused MXFP8 product, load-balance
+loss); ``api`` and ``block_ops`` are
 its thin Python binding and ``workloads``
 the seeded synthetic inputs.  Importing ``api`` functions loads the library
 lazily and raises if it has not been built.
@@ -18,4 +20,8 @@ from .api import (  # noqa: F401
     mxfp8_linear_workspace_size, set_gemm_2sm, set_gemm_chain, W4A4MoELayer, moe_forward_w4a4_mma_scales,
     MXFP4Linear, mxfp4_linear, mxfp4_linear_mma_scales, moe_router_gate_topk,
     mx_dequantize_bf16_2d, moe_forward_mxfp8_gated_mma_scales,
+)
+from .block_ops import (  # noqa: F401
+    MXFP8FusedLinear, moe_balance_loss, moe_balance_loss_workspace_size, mx_add_rmsnorm_quant,
+    mxfp8_linear_fused, mxfp8_linear_fused_workspace_size,
 )

@@ -1,0 +1,295 @@
+"""Binding of the operators around the expert forward: the RMS norm with MXFP8
+output, the fused MXFP8 product and the router's load-balance loss.
+
+Like ``api``: argument marshalling only, every step runs in the library's
+kernels.  An MXFP8 activation is a pair ``(q, s)``: e4m3 payload uint8 [.., K]
+and its scales in the tensor-core layout, an opaque uint8 array
+[ceil(M/128) * 128, ceil(K/128) * 4].
+"""
+
+from __future__ import annotations
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+from .api import _need, _u8, mx_quantize_3d, mx_scales_to_mma_layout
+
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _stream(t):
+    """The current stream of the tensor's device, as an integer handle."""
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _rows(t, name, dtypes, aligned=False):
+    """A CUDA tensor of one of ``dtypes``, contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+_HALF_OR_FLOAT = (torch.bfloat16, torch.float32)
+
+
+def _mma_scale_shape(M: int, K: int):
+    return (-(-M // 128) * 128, -(-K // 128) * 4)
+
+
+def mx_add_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, bf16_out: bool = False,
+                         mma_scales: bool = False, residual_out=None) -> dict:
+    """h = x + residual; y = bf16(h * weight / sqrt(mean(h^2) + eps)); MXFP8 of y.
+
+    x bf16 [.., H] (contiguous, or 2D with rows further apart), weight bf16 or
+    fp32 [H], residual bf16 or fp32 [.., H].  Returns ``q`` (e4m3 codes uint8
+    [.., H]), ``s`` (e8m0 uint8 [.., ceil(H/32)], or the tensor-core layout
+    with ``mma_scales``: what ``mxfp8_linear_fused`` reads), ``y`` (bf16,
+    with ``bf16_out``: what the router reads) and ``residual`` (h in the
+    residual's type; pass ``residual_out=residual`` to update it in place)."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise TypeError("x must be a torch.Tensor of at least one dimension")
+    H = x.shape[-1]
+    ldx = H
+    if x.dim() == 2 and x.stride(1) == 1 and x.is_cuda and x.dtype == torch.bfloat16:
+        ldx = x.stride(0) if x.shape[0] > 1 else H
+    else:
+        _rows(x, "x", (torch.bfloat16,))
+    if ldx < H:
+        raise ValueError("x: overlapping rows")
+    _rows(weight, "weight", _HALF_OR_FLOAT)
+    if weight.dim() != 1 or weight.shape[0] != H:
+        raise ValueError(f"weight is {tuple(weight.shape)}, x has H = {H}")
+    dev, shape = x.device, x.shape
+    M = x.numel() // H if H else 0
+    out = {}
+    res_ptr = res_out_ptr = None
+    if residual is not None:
+        _rows(residual, "residual", _HALF_OR_FLOAT)
+        if residual.shape != shape:
+            raise ValueError(f"residual is {tuple(residual.shape)}, x is {tuple(shape)}")
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        else:
+            _rows(residual_out, "residual_out", (residual.dtype,))
+            if residual_out.shape != shape:
+                raise ValueError(f"residual_out is {tuple(residual_out.shape)}, x is {tuple(shape)}")
+        res_ptr, res_out_ptr = residual.data_ptr(), residual_out.data_ptr()
+        out["residual"] = residual_out
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    q = torch.empty(shape, dtype=torch.uint8, device=dev)
+    s = torch.empty(_mma_scale_shape(M, H) if mma_scales else shape[:-1] + (-(-H // 32),),
+                    dtype=torch.uint8, device=dev)
+    out["q"], out["s"] = q, s
+    y_ptr = None
+    if bf16_out:
+        out["y"] = y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        y_ptr = y.data_ptr()
+    rc = _lib.load().mx_add_rmsnorm_quant(
+        x.data_ptr(), ldx, res_ptr, residual is not None and residual.dtype == torch.float32,
+        res_out_ptr, weight.data_ptr(), weight.dtype == torch.float32, eps, M, H, y_ptr,
+        q.data_ptr(), s.data_ptr(), mma_scales, _stream(x))
+    if rc:
+        _lib.check("mx_add_rmsnorm_quant", rc)
+    return out
+
+
+def mxfp8_linear_fused_workspace_size(M: int, K: int) -> int:
+    return int(_lib.load().mxfp8_linear_fused_workspace_size(M, K))
+
+
+def mxfp8_linear_fused(x, wq, ws_mma, bias=None, act=None, residual=None, mx_out: bool = False,
+                       out=None, workspace=None):
+    """act(x . wq^T + bias) + residual with an MXFP8 product.
+
+    x: bf16 [.., K] (MX-quantized per token on the device) or an MXFP8 pair
+    (q, s) with tensor-core scales; wq e4m3 [N, K], ws_mma its scales in the
+    tensor-core layout; bias bf16 or fp32 [N]; act one of "none", "relu",
+    "gelu", "gelu_tanh", "silu"; residual bf16 [.., N].  Returns bf16 [.., N],
+    or with ``mx_out`` the MXFP8 pair of act(..) (no residual)."""
+    xq = xs = x_ptr = xq_ptr = xs_ptr = ws_ptr = None
+    ws_bytes = 0
+    if isinstance(x, tuple):
+        xq, xs = x
+        xq = _u8(xq)
+        _rows(xq, "x[0]", (torch.uint8,))
+        _rows(xs, "x[1]", (torch.uint8,))
+        xin = xq
+    else:
+        _rows(x, "x", (torch.bfloat16,))
+        xin = x
+    wq = _u8(wq)
+    _need(wq, "wq", torch.uint8, 2)
+    _rows(ws_mma, "ws_mma", (torch.uint8,))
+    N, K = wq.shape
+    if xin.dim() < 1 or xin.shape[-1] != K:
+        raise ValueError(f"wq is {tuple(wq.shape)}, x is {tuple(xin.shape)}")
+    M = xin.numel() // K if K else 0
+    if ws_mma.numel() != _mma_scale_shape(N, K)[0] * _mma_scale_shape(N, K)[1]:
+        raise ValueError("ws_mma is not in the tensor-core layout of wq's scales")
+    if xq is not None:
+        if xs.numel() != _mma_scale_shape(M, K)[0] * _mma_scale_shape(M, K)[1]:
+            raise ValueError("x's scales are not in the tensor-core layout")
+        xq_ptr, xs_ptr = xq.data_ptr(), xs.data_ptr()
+    else:
+        x_ptr = x.data_ptr()
+        need = mxfp8_linear_fused_workspace_size(M, K)
+        if workspace is None:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act: expected one of {sorted(k for k in ACTIVATIONS if k)}, got {act!r}")
+    bias_ptr, bias32 = None, 0
+    if bias is not None:
+        _rows(bias, "bias", _HALF_OR_FLOAT)
+        if bias.dim() != 1 or bias.shape[0] != N:
+            raise ValueError(f"bias is {tuple(bias.shape)}, wq has N = {N}")
+        bias_ptr, bias32 = bias.data_ptr(), bias.dtype == torch.float32
+    shape = xin.shape[:-1] + (N,)
+    res_ptr = None
+    if residual is not None:
+        if mx_out:
+            raise ValueError("an MXFP8 result takes no residual")
+        _rows(residual, "residual", (torch.bfloat16,))
+        if residual.shape != shape:
+            raise ValueError(f"residual is {tuple(residual.shape)}, the result {tuple(shape)}")
+        res_ptr = residual.data_ptr()
+    out_ptr = oq_ptr = os_ptr = None
+    if mx_out:
+        if out is not None:
+            raise ValueError("out holds a bf16 result")
+        oq = torch.empty(shape, dtype=torch.uint8, device=xin.device)
+        os_ = torch.empty(_mma_scale_shape(M, N), dtype=torch.uint8, device=xin.device)
+        oq_ptr, os_ptr = oq.data_ptr(), os_.data_ptr()
+    else:
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=xin.device)
+        else:
+            _rows(out, "out", (torch.bfloat16,))
+            if out.shape != shape:
+                raise ValueError(f"out is {tuple(out.shape)}, the result {tuple(shape)}")
+        out_ptr = out.data_ptr()
+    rc = _lib.load().mxfp8_linear_fused(
+        x_ptr, xq_ptr, xs_ptr, wq.data_ptr(), ws_mma.data_ptr(), M, N, K, bias_ptr, bias32,
+        ACTIVATIONS[act], res_ptr, out_ptr, oq_ptr, os_ptr, ws_ptr, ws_bytes, _stream(xin))
+    if rc:
+        _lib.check("mxfp8_linear_fused", rc)
+    return (oq, os_) if mx_out else out
+
+
+class MXFP8FusedLinear:
+    """An MXFP8 linear with bias and activation, and the residual's addition.
+
+    Weights as ``MXFP8Linear``: ``from_bf16`` quantizes at load, the
+    constructor takes an offline checkpoint's payload and [N, ceil(K/32)]
+    scales, which are re-laid once.  Calls take bf16 rows or an MXFP8 pair."""
+
+    def __init__(self, wq, ws, bias=None, act=None):
+        self.wq = _u8(wq)
+        self.N, self.K = self.wq.shape
+        self.ws_mma = mx_scales_to_mma_layout(ws, self.K)
+        self.bias, self.act = bias, act
+        self._ws = None
+
+    @classmethod
+    def from_bf16(cls, w, bias=None, act=None):
+        return cls(*mx_quantize_3d(w), bias=bias, act=act)
+
+    def workspace(self, M: int, device):
+        need = mxfp8_linear_fused_workspace_size(M, self.K)
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        return self._ws
+
+    def __call__(self, x, residual=None, mx_out: bool = False, out=None):
+        ws = None
+        if not isinstance(x, tuple) and x.is_cuda:
+            ws = self.workspace(x.numel() // self.K, x.device)
+        return mxfp8_linear_fused(x, self.wq, self.ws_mma, self.bias, self.act, residual, mx_out,
+                                  out, ws)
+
+
+def moe_balance_loss_workspace_size(T: int, E: int) -> int:
+    return int(_lib.load().moe_balance_loss_workspace_size(T, E))
+
+
+def _balance(logits, topk_ids, mask, counts, coef, grad):
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor (the library has no CPU path)")
+    if logits.dtype != torch.float32 or logits.dim() != 2:
+        raise TypeError("logits: expected fp32 [T, E]")
+    T, E = logits.shape
+    if E > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: a row must be contiguous")
+    ldl = logits.stride(0) if T > 1 else E
+    if ldl < E:
+        raise ValueError("logits: overlapping rows")
+    _need(topk_ids, "topk_ids", torch.int32, 2)
+    if topk_ids.shape[0] != T:
+        raise ValueError("logits and topk_ids disagree on T")
+    mask_ptr = counts_ptr = grad_ptr = None
+    if mask is not None:
+        _rows(mask, "mask", (torch.bool, torch.uint8))
+        if mask.shape != (T,):
+            raise ValueError(f"mask is {tuple(mask.shape)}, logits have T = {T}")
+        mask_ptr = mask.data_ptr()
+    if counts is not None:
+        _rows(counts, "counts", (torch.int64,))
+        if counts.shape != (E,):
+            raise ValueError(f"counts is {tuple(counts.shape)}, logits have E = {E}")
+        counts_ptr = counts.data_ptr()
+    dev = logits.device
+    lib = _lib.load()
+    ws = torch.empty(lib.moe_balance_loss_workspace_size(T, E), dtype=torch.uint8, device=dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    own_counts = torch.empty(E, dtype=torch.int64, device=dev)
+    out = {"loss": loss, "counts": own_counts}
+    if grad:
+        out["dlogits"] = d = torch.empty((T, E), dtype=torch.float32, device=dev)
+        grad_ptr = d.data_ptr()
+    rc = lib.moe_balance_loss(
+        logits.data_ptr(), ldl, topk_ids.data_ptr(), mask_ptr, counts_ptr, T, E,
+        topk_ids.shape[1], coef, loss.data_ptr(), own_counts.data_ptr(), grad_ptr, ws.data_ptr(),
+        ws.numel(), _stream(logits))
+    if rc:
+        _lib.check("moe_balance_loss", rc)
+    return out
+
+
+class _BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, topk_ids, mask, counts, coef):
+        r = _balance(logits, topk_ids, mask, counts, coef, True)
+        ctx.save_for_backward(r["dlogits"])
+        ctx.mark_non_differentiable(r["counts"])
+        return r["loss"], r["counts"]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, _):
+        return ctx.saved_tensors[0] * dloss, None, None, None, None
+
+
+def moe_balance_loss(logits, topk_ids, mask=None, counts=None, coef: float = 1.0,
+                     grad: bool = False) -> dict:
+    """The router's load-balance loss coef * E * sum_e f_e mean_t p_te.
+
+    logits fp32 [T, E] (rows may be further apart), topk_ids int32 [T, k] (of
+    ``moe_router_gate_topk``), mask bool or uint8 [T] (True: the token counts),
+    counts int64 [E] to take f from instead of this call's own (e.g. summed
+    over micro-batches or ranks).  Returns ``loss`` (fp32 scalar) and ``counts``
+    (int64 [E], this call's).  The loss and its gradient come from one pass:
+    with ``grad`` the result holds ``dlogits`` fp32 [T, E]; without it, and
+    with logits that require a gradient, ``loss`` is differentiable by
+    autograd (once)."""
+    if not grad and isinstance(logits, torch.Tensor) and logits.requires_grad \
+            and torch.is_grad_enabled():
+        loss, own = _BalanceLoss.apply(logits, topk_ids, mask, counts, float(coef))
+        return {"loss": loss, "counts": own}
+    return _balance(logits, topk_ids, mask, counts, float(coef), grad)

@@ -673,6 +673,105 @@ mxmoe_status mxfp4_linear_mma_scales(const uint16_t* x, const uint8_t* wp, const
   return linear_impl(x, wp, ws_mma, true, M, N, K, out, workspace, ws_bytes, stream, true);
 }
 
+// ---------------------------------------------------------------- around the experts
+
+static inline bool aligned(const void* p, unsigned bytes) {
+  return ((uintptr_t)p & (bytes - 1)) == 0;
+}
+
+mxmoe_status mx_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* residual,
+                                  int residual_fp32, void* residual_out, const void* weight,
+                                  int weight_fp32, float eps, int64_t M, int64_t H, uint16_t* y,
+                                  uint8_t* q, uint8_t* scale, int mma_layout, void* stream) {
+  if (M < 0 || M >= (1ll << 31) || H <= 0 || H % 16 != 0 || ldx < H || !(eps >= 0.f))
+    return MXMOE_ERR_SHAPE;
+  if (H > 32768) return MXMOE_ERR_UNSUPPORTED;
+  if (M == 0) return MXMOE_OK;
+  MXMOE_CHECK_PTR(x);
+  MXMOE_CHECK_PTR(weight);
+  MXMOE_CHECK_PTR(q);
+  MXMOE_CHECK_PTR(scale);
+  if ((residual == nullptr) != (residual_out == nullptr)) return MXMOE_ERR_NULL;
+  if (ldx % 8 != 0 || !aligned(weight, 32) || !aligned(residual, 32) ||
+      !aligned(residual_out, 32) || !aligned(y, 32))
+    return MXMOE_ERR_ALIGN;
+  return from_cuda(launch_add_rmsnorm_quant(x, ldx, residual, residual_fp32 != 0, residual_out,
+                                            weight, weight_fp32 != 0, eps, M, (int)H, y, q, scale,
+                                            mma_layout != 0, (cudaStream_t)stream));
+}
+
+// Workspace of mxfp8_linear_fused with bf16 input: xq [M, K] | xs in the MMA layout.
+static size_t fused_xs_offset(int64_t M, int64_t K) { return align256((size_t)M * K); }
+
+size_t mxfp8_linear_fused_workspace_size(int64_t M, int64_t K) {
+  if (!linear_shape_ok(M, 16, K) || M >= (1ll << 24)) return 0;
+  return fused_xs_offset(M, K) +
+         align256((size_t)((M + 127) / 128) * (size_t)((K + 127) / 128) * 512);
+}
+
+mxmoe_status mxfp8_linear_fused(const uint16_t* x, const uint8_t* xq, const uint8_t* xs,
+                                const uint8_t* wq, const uint8_t* ws, int64_t M, int64_t N,
+                                int64_t K, const void* bias, int bias_fp32, int act,
+                                const uint16_t* residual, uint16_t* out, uint8_t* out_q,
+                                uint8_t* out_s, void* workspace, size_t ws_bytes, void* stream) {
+  if (!linear_shape_ok(M, N, K) || M >= (1ll << 24) || act < 0 || act >= ACT_COUNT)
+    return MXMOE_ERR_SHAPE;
+  // one output form; the residual joins a bf16 result only
+  if (out && (out_q || out_s)) return MXMOE_ERR_UNSUPPORTED;
+  if (residual && !out) return MXMOE_ERR_UNSUPPORTED;
+  if (M == 0) return MXMOE_OK;
+  MXMOE_CHECK_PTR(wq);
+  MXMOE_CHECK_PTR(ws);
+  if (bias) MXMOE_CHECK_PTR(bias);
+  if (residual) MXMOE_CHECK_PTR(residual);
+  if (out) {
+    MXMOE_CHECK_PTR(out);
+  } else {
+    MXMOE_CHECK_PTR(out_q);
+    MXMOE_CHECK_PTR(out_s);
+  }
+  cudaStream_t st = (cudaStream_t)stream;
+  if (x) {
+    if (xq || xs) return MXMOE_ERR_UNSUPPORTED;  // one input form
+    MXMOE_CHECK_PTR(x);
+    if (!workspace || ws_bytes < mxfp8_linear_fused_workspace_size(M, K))
+      return MXMOE_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MXMOE_ERR_ALIGN;
+    uint8_t* base = (uint8_t*)workspace;
+    if (launch_mx_quantize_tiled(x, M, K, base, base + fused_xs_offset(M, K), nullptr, st) !=
+        cudaSuccess)
+      return MXMOE_ERR_CUDA;
+    xq = base;
+    xs = base + fused_xs_offset(M, K);
+  } else {
+    MXMOE_CHECK_PTR(xq);
+    MXMOE_CHECK_PTR(xs);
+  }
+  return from_cuda(launch_linear_fused(xq, xs, wq, ws, M, (int)N, (int)K, bias, bias_fp32 != 0,
+                                       act, residual, out, out_q, out_s, st));
+}
+
+size_t moe_balance_loss_workspace_size(int64_t T, int E) {
+  if (T < 0 || E < 1 || E > 1024) return 0;
+  return balance_workspace_bytes(T, E);
+}
+
+mxmoe_status moe_balance_loss(const float* logits, int64_t ldl, const int32_t* topk_ids,
+                              const uint8_t* mask, const int64_t* counts_in, int64_t T, int E,
+                              int k, float coef, float* loss, int64_t* counts, float* dlogits,
+                              void* ws, size_t ws_bytes, void* stream) {
+  if (T < 0 || E < 1 || k < 1 || k > E || ldl < E) return MXMOE_ERR_SHAPE;
+  if (E > 1024 || k > 32) return MXMOE_ERR_UNSUPPORTED;
+  if (T >= (1ll << 31) || T * k >= (1ll << 31)) return MXMOE_ERR_SHAPE;
+  if (!loss || !counts || (T > 0 && (!logits || !topk_ids))) return MXMOE_ERR_NULL;
+  if (!aligned(loss, 4) || !aligned(counts, 8) || !aligned(logits, 4) || !aligned(topk_ids, 4) ||
+      !aligned(counts_in, 8) || !aligned(dlogits, 4) || !aligned16(ws))
+    return MXMOE_ERR_ALIGN;
+  if (!ws || ws_bytes < balance_workspace_bytes(T, E)) return MXMOE_ERR_WORKSPACE;
+  return from_cuda(launch_balance_loss(logits, ldl, topk_ids, mask, counts_in, T, E, k, coef, loss,
+                                       counts, dlogits, (uint32_t*)ws, (cudaStream_t)stream));
+}
+
 // ---------------------------------------------------------------- host-buffer layer
 
 // Device staging of one chunk slot: x | logits | out | layer workspace.

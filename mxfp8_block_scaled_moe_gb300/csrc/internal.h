@@ -128,6 +128,29 @@ cudaError_t launch_gemm_chain(const uint8_t* xq, const uint8_t* xs, const uint8_
 // than the MXFP8 count for the same shape).
 int gemm_bf16_ksplit(int64_t M, int N, int K, bool packed_fp4 = false);
 
+// Residual addition + RMS norm + MXFP8 rows (norm.cu).  res (nullable) bf16,
+// fp32 with res32; w fp32 with w32; y nullable; ldx in elements.
+cudaError_t launch_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* res, bool res32,
+                                     void* res_out, const void* w, bool w32, float eps, int64_t M,
+                                     int H, uint16_t* y, uint8_t* q, uint8_t* s, bool tiled,
+                                     cudaStream_t stream);
+
+// MXFP8 product with bias, activation and residual (linear.cu).  Scales in the
+// MMA layout; bias, residual nullable; either out (bf16) or oq / os (MXFP8).
+enum : int { ACT_NONE = 0, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU, ACT_COUNT };
+cudaError_t launch_linear_fused(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq,
+                                const uint8_t* ws, int64_t M, int N, int K, const void* bias,
+                                bool bias32, int act, const uint16_t* residual, uint16_t* out,
+                                uint8_t* oq, uint8_t* os, cudaStream_t stream);
+
+// Load-balance loss, counts and the logits' gradient (balance.cu).  mask,
+// counts_in, dlogits nullable.
+size_t balance_workspace_bytes(int64_t T, int E);
+cudaError_t launch_balance_loss(const float* logits, int64_t ldl, const int32_t* ids,
+                                const uint8_t* mask, const int64_t* counts_in, int64_t T, int E,
+                                int k, float coef, float* loss, int64_t* counts, float* dlogits,
+                                uint32_t* ws, cudaStream_t stream);
+
 // [rows, ceil(K/32)] scales -> tiled layout with KT = ceil(K/128); rows and
 // slots past the data (a ragged row block or K slice) are written as 127.
 cudaError_t launch_scales_to_tiled(const uint8_t* scale, int64_t rows, int64_t K, uint8_t* out,

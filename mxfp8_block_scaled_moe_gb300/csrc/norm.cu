@@ -1,0 +1,235 @@
+// Residual addition + root-mean-square norm + MXFP8 quantization of the rows
+// that the next product reads.
+//
+//   h = x + residual          rounded to the residual's type (bf16 or fp32)
+//   y = bf16(h * w / sqrt(mean(h^2) + eps))
+//   q, s = MX-quant(y)        the rule of mx_quantize_3d (common.cuh)
+//
+// The norm reads h as it is stored, so the statistics can be recomputed from
+// the stored residual stream; y is rounded to bf16 before the quantization
+// (a second rounding, 2^-9 relative against the payload's 2^-4), so that q, s
+// are the bytes of mx_quantize_3d(y) and the router, which reads y, and the
+// products, which read q, see the same rows.  The sum of squares is fp32.
+//
+// One group of warps per row, 16 elements (half an MX block) per thread and
+// chunk, the row held in registers between the sum and the output: x and the
+// residual are read once, every output written once.
+//
+// Roofline: HBM-bound for many rows, latency-bound for a few.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tiled_scales.h"
+
+namespace mxmoe {
+namespace norm {
+
+constexpr int kChunk = 16;  // elements per thread and chunk
+
+struct Params {
+  const uint16_t* x;
+  int64_t ldx;
+  const void* res;
+  void* res_out;
+  const void* w;
+  float eps;
+  int64_t M;
+  int H, wpr;  // row length, warps per row
+  uint16_t* y;
+  uint8_t* q;
+  uint8_t* s;
+  bool w32, tiled, x32;  // fp32 weight, tiled scales, 32-byte aligned x rows
+};
+
+__device__ __forceinline__ void load16(const uint16_t* p, bool v32, uint32_t (&w)[8]) {
+  if (v32) {
+    ld_nc_v8(p, w);
+  } else {
+    const uint4 a = ld_nc_v4(p), b = ld_nc_v4(p + 8);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+}
+
+// The residual may be updated in place, so its loads are ordinary ones (each
+// element is read and then written by the same thread).
+__device__ __forceinline__ void load32b(const void* p, uint32_t (&r)[8]) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "l"(p)
+               : "memory");
+}
+
+// kRes: 0 no residual, 1 bf16, 2 fp32.  CPT chunks per thread.
+template <int CPT, int kRes>
+__global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const Params p) {
+  __shared__ float s_red[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tpr = 32 * p.wpr;  // threads per row
+  const int rl = threadIdx.x / tpr, t = threadIdx.x - rl * tpr;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + rl;
+  const bool row_ok = row < p.M;
+  const int nch = p.H / kChunk;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  float h[CPT][kChunk];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = t + i * tpr;
+    const bool in = row_ok && c < nch;
+    uint32_t xw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (in) load16(p.x + row * p.ldx + c * kChunk, p.x32, xw);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      h[i][2 * j] = bf16_bits_to_float(xw[j] & 0xFFFFu);
+      h[i][2 * j + 1] = bf16_bits_to_float(xw[j] >> 16);
+    }
+    if (in && kRes == 1) {
+      const int64_t at = row * p.H + c * kChunk;
+      uint32_t rw[8];
+      load32b(static_cast<const uint16_t*>(p.res) + at, rw);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        rw[j] = cvt_bf16x2(h[i][2 * j] + bf16_bits_to_float(rw[j] & 0xFFFFu),
+                           h[i][2 * j + 1] + bf16_bits_to_float(rw[j] >> 16));
+        h[i][2 * j] = bf16_bits_to_float(rw[j] & 0xFFFFu);
+        h[i][2 * j + 1] = bf16_bits_to_float(rw[j] >> 16);
+      }
+      st_v8(static_cast<uint16_t*>(p.res_out) + at, rw);
+    }
+    if (in && kRes == 2) {
+      const int64_t at = row * p.H + c * kChunk;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t rw[8];
+        load32b(static_cast<const float*>(p.res) + at + 8 * half, rw);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          h[i][8 * half + j] += __uint_as_float(rw[j]);
+          rw[j] = __float_as_uint(h[i][8 * half + j]);
+        }
+        st_v8(static_cast<float*>(p.res_out) + at + 8 * half, rw);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  if (p.wpr > 1) {  // uniform over the grid
+    if (lane == 0) s_red[warp] = ss;
+    __syncthreads();
+    ss = lane < p.wpr ? s_red[rl * p.wpr + lane] : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  }
+  const float r = rsqrtf(ss / (float)p.H + p.eps);
+
+  const int nbr = (p.H + 31) / 32, KT = (p.H + 127) / 128;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = t + i * tpr;
+    const bool in = row_ok && c < nch;
+    uint32_t yw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (in) {
+      if (p.w32) {
+        uint32_t wv[8];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          ld_nc_v8(static_cast<const float*>(p.w) + c * kChunk + 8 * half, wv);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            yw[4 * half + j] = cvt_bf16x2(h[i][8 * half + 2 * j] * r * __uint_as_float(wv[2 * j]),
+                                          h[i][8 * half + 2 * j + 1] * r *
+                                              __uint_as_float(wv[2 * j + 1]));
+        }
+      } else {
+        uint32_t wv[8];
+        ld_nc_v8(static_cast<const uint16_t*>(p.w) + c * kChunk, wv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          yw[j] = cvt_bf16x2(h[i][2 * j] * r * bf16_bits_to_float(wv[j] & 0xFFFFu),
+                             h[i][2 * j + 1] * r * bf16_bits_to_float(wv[j] >> 16));
+      }
+      if (p.y) st_v8(p.y + row * p.H + c * kChunk, yw);
+    }
+    // the block's other half is the neighbouring lane's (absent halves are 0)
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = umax(m, bf16x2_absmax_bits(yw[j]));
+    m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const uint32_t sb = e8m0_from_amax_bits(m);
+    if (in) {
+      const float inv = inv_scale_from_e8m0(sb);
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = cvt_e4m3x4(bf16_bits_to_float(yw[2 * j] & 0xFFFFu) * inv,
+                          bf16_bits_to_float(yw[2 * j] >> 16) * inv,
+                          bf16_bits_to_float(yw[2 * j + 1] & 0xFFFFu) * inv,
+                          bf16_bits_to_float(yw[2 * j + 1] >> 16) * inv);
+      st_v4(p.q + row * p.H + c * kChunk, make_uint4(o[0], o[1], o[2], o[3]));
+    }
+    // four blocks' scale bytes (eight lanes) go out as one word; a slot past
+    // the row's last block holds 127 (scale 1) in the tiled layout
+    const int j0 = c >> 1;
+    const uint32_t byte = j0 < nbr ? sb : 127u;
+    uint32_t word = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      word |= __shfl_sync(0xffffffffu, byte, (lane & ~7) + 2 * b) << (8 * b);
+    if (in && p.tiled) {
+      if ((c & 7) == 0)
+        *reinterpret_cast<uint32_t*>(p.s + tiled_scale_offset(row, j0, KT)) = word;
+    } else if (in && (nbr & 3) == 0) {
+      if ((c & 7) == 0) *reinterpret_cast<uint32_t*>(p.s + row * nbr + j0) = word;
+    } else if (in && (c & 1) == 0) {
+      p.s[row * nbr + j0] = (uint8_t)sb;
+    }
+  }
+}
+
+}  // namespace norm
+
+cudaError_t launch_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* res, bool res32,
+                                     void* res_out, const void* w, bool w32, float eps, int64_t M,
+                                     int H, uint16_t* y, uint8_t* q, uint8_t* s, bool tiled,
+                                     cudaStream_t stream) {
+  using namespace norm;
+  if (M == 0) return cudaSuccess;
+  Params p;
+  p.x = x;
+  p.ldx = ldx;
+  p.res = res;
+  p.res_out = res_out;
+  p.w = w;
+  p.eps = eps;
+  p.M = M;
+  p.H = H;
+  p.y = y;
+  p.q = q;
+  p.s = s;
+  p.w32 = w32;
+  p.tiled = tiled;
+  p.x32 = ((uintptr_t)x & 31u) == 0 && ldx % 16 == 0;
+  const int nch = H / kChunk;
+  const int cpt = nch > 1024 ? 2 : 1;
+  p.wpr = (int)ceil_div(nch, 32 * cpt);
+  const int rows = std::max(1, 8 / p.wpr);
+  const int64_t grid = ceil_div(M, rows);
+  const dim3 block(32 * p.wpr * rows);
+  const int kind = !res ? 0 : res32 ? 2 : 1;
+  auto kern = cpt == 1 ? (kind == 0   ? add_rmsnorm_quant_kernel<1, 0>
+                          : kind == 1 ? add_rmsnorm_quant_kernel<1, 1>
+                                      : add_rmsnorm_quant_kernel<1, 2>)
+                       : (kind == 0   ? add_rmsnorm_quant_kernel<2, 0>
+                          : kind == 1 ? add_rmsnorm_quant_kernel<2, 1>
+                                      : add_rmsnorm_quant_kernel<2, 2>);
+  return launch_pdl(kern, dim3((unsigned)grid), block, 0, stream, p);
+}
+
+}  // namespace mxmoe
