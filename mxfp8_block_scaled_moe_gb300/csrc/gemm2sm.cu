@@ -31,6 +31,7 @@
 // Each CTA's TMEM holds the scales of its own 128 A rows and of all 256 B
 // rows (both CTAs stage the B rows' scale chunks).
 #include "gemm_common.cuh"
+#include "gemm_pair.cuh"
 
 namespace mxmoe {
 namespace gemm {
@@ -62,76 +63,6 @@ struct Layout2 {
   static_assert(ALLOC <= 232448, "shared memory");
   static_assert(SF_COL0 + 2 * SEG2_COLS <= TMEM_COLS, "tensor memory");
 };
-
-// ---------------------------------------------------------------- cta_group::2 PTX
-
-// TMA tile load into this CTA's shared memory that completes on an mbarrier
-// of either CTA of the pair (`bar` is a shared::cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0,
-                                                 int c1, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// Bounded wait with cluster-scope acquire (arrivals come from both CTAs).
-__device__ __forceinline__ bool wait_bar_cluster(uint32_t bar, uint32_t parity, long long limit,
-                                                 int* status, volatile int* abort_flag) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (!mbar_try_wait_cluster(bar, parity)) {
-    if (*abort_flag) return false;
-    if (clock64() - t0 > limit) {
-      report_error(status, ERR_TIMEOUT);
-      *abort_flag = 1;
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ void tc2_mma_mxf4(uint32_t d, uint64_t adesc, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
-      " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
-      : "memory");
-}
-__device__ __forceinline__ void tc2_mma_mxf8(uint32_t d, uint64_t adesc, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
-      " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
-      : "memory");
-}
-// Arrive on the barrier at `bar`'s offset in both CTAs once all prior
-// tcgen05 operations of this thread have completed.
-__device__ __forceinline__ void tc2_commit_both(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)0x3)
-      : "memory");
-}
 
 template <bool kSwiglu, int kFmt>
 __global__ void __launch_bounds__(THREADS1, 1)

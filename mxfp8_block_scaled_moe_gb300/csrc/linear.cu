@@ -20,12 +20,10 @@
 // all warps the epilogue (a warp per token, 4 columns of n per lane).
 //
 // Every mbarrier wait is bounded as in gemm.cu.
-#include "gemm_common.cuh"
+#include "linear.cuh"
 
 namespace mxmoe {
 namespace linear {
-
-using namespace gemm;
 
 constexpr int WM = 128;              // weight rows per CTA
 constexpr int W_BYTES = WM * BK;     // 16 KB per k-slice
@@ -34,22 +32,6 @@ constexpr int L_THREADS = 32 * WARPS;
 constexpr int DRAIN_WARPS = 8;       // accumulator -> shared memory
 constexpr int MAX_STAGES = 6;
 constexpr int MAX_SPLIT = 8;
-
-struct LinParams {
-  const uint8_t* sfw;      // weight scales, MMA layout [ceil(N/128)][KT] chunks
-  const uint8_t* sfx;      // activation scales, MMA layout
-  const void* bias;        // [N] or null
-  const uint16_t* res;     // [M, N] bf16 or null
-  uint16_t* out;           // [M, N] bf16 (bf16 output)
-  uint8_t* oq;             // [M, N] e4m3 (MXFP8 output)
-  uint8_t* os;             // MMA layout, KT_out = ceil(N/128)
-  int64_t M;
-  int N, K, act;
-  bool bias32;
-  int NT, stages, nsplit;
-  int* status;
-  long long wait_limit;
-};
 
 // Shared-memory layout (runtime NT and stage count).
 struct Smem {
@@ -92,23 +74,6 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-// act(z).  silu(z) = z / (1 + e^-z); (1 + tanh u) / 2 = 1 / (1 + e^-2u), so
-// the tanh form of gelu is z / (1 + e^-2u) with the same two hardware
-// functions; erfcf (CUDA's) keeps gelu's relative accuracy where 1 + erf
-// cancels.
-constexpr float kGeluTanh = -2.f * 0.7978845608f * 1.4426950409f;  // -2 sqrt(2 / pi) log2 e
-
-__device__ __forceinline__ float activate(int act, float z) {
-  switch (act) {
-    case ACT_RELU: return fmaxf(z, 0.f);
-    case ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678f);
-    case ACT_GELU_TANH:
-      return z * rcp_approx(1.f + ex2_approx(kGeluTanh * (z + 0.044715f * z * z * z)));
-    case ACT_SILU: return swiglu(z, 1.f);
-    default: return z;
-  }
-}
-
 // A token's 4 columns n .. n + 3 (n + 3 < N) of this lane: bias, activation,
 // residual, store.  bias: the lane's 4 values.  Called by a whole warp on one
 // token t; lane l holds columns n0 + 4 l.
@@ -117,8 +82,7 @@ __device__ __forceinline__ void finish_token(const LinParams& p, int64_t t, int 
   const int n = n0 + 4 * lane;
   const bool in = n < p.N;
   float a[4] = {v.x + bias.x, v.y + bias.y, v.z + bias.z, v.w + bias.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = activate(p.act, a[i]);
+  activate_all(p.act, a);
   if (p.out) {
     if (!in) return;
     a[0] += bf16_bits_to_float(res.x & 0xFFFFu);
@@ -401,12 +365,7 @@ cudaError_t launch_linear_fused(const uint8_t* xq, const uint8_t* xs, const uint
     if (err != cudaSuccess) return err;
     configured[dev] = context_id();
   }
-  const Plan pl = make_plan(M, N, K);
-  CUtensorMap tmW, tmX;
-  if (!make_map(&tmW, wq, (uint64_t)K, (uint64_t)N, BK, WM) ||
-      !make_map(&tmX, xq, (uint64_t)K, (uint64_t)M, BK, (uint32_t)pl.NT))
-    return cudaErrorInvalidValue;
-  LinParams p;
+  LinParams p = {};
   p.sfw = ws;
   p.sfx = xs;
   p.bias = bias;
@@ -419,11 +378,21 @@ cudaError_t launch_linear_fused(const uint8_t* xq, const uint8_t* xs, const uint
   p.K = K;
   p.act = act;
   p.bias32 = bias32;
+  p.status = device_status_ptr();
+  p.wait_limit = wait_limit_cycles();
+  if (M > 256) {
+    pair_cycles(M, N, K, &p.BN);
+    const cudaError_t err = launch_pair(xq, wq, p, stream);
+    if (err != cudaErrorNotSupported) return err;
+  }
+  const Plan pl = make_plan(M, N, K);
+  CUtensorMap tmW, tmX;
+  if (!make_map(&tmW, wq, (uint64_t)K, (uint64_t)N, BK, WM) ||
+      !make_map(&tmX, xq, (uint64_t)K, (uint64_t)M, BK, (uint32_t)pl.NT))
+    return cudaErrorInvalidValue;
   p.NT = pl.NT;
   p.stages = pl.stages;
   p.nsplit = pl.nsplit;
-  p.status = device_status_ptr();
-  p.wait_limit = wait_limit_cycles();
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -1,0 +1,480 @@
+// The fused MXFP8 product for many rows: CTA pairs (tcgen05 cta_group::2) and
+// two accumulators in tensor memory.
+//
+// A pair of CTAs on two SMs computes 256 rows x BN columns (BN = 224, 192 or
+// 128): CTA r holds 128 rows of x and half of the BN weight rows, one
+// tcgen05.mma (M = 256, N = BN, K = 32) issued by the even CTA reads both
+// CTAs' operands and accumulates each CTA's 128 rows in its own TMEM.
+//
+// What bounds it.  An MMA of N columns takes N / 2 tensor cycles; meanwhile each
+// SM's shared memory serves the operands (128 rows of A and N rows of B, 32
+// bytes each) and takes in what TMA writes for the next ones (128 + N / 2
+// rows): (384 + 1.5 N) * 32 B at 128 B per cycle is 160 cycles at N = 256,
+// 144 at 224, more than the tensor cycles (128, 112).  BN = 224 instead of 256
+// costs 3% of that rate and leaves 64 of the 512 TMEM columns beside two
+// accumulators: the scale factors take a ring of four k-slices there, and the
+// epilogue of a tile (bias, activation, residual, stores) runs under the next
+// tile's MMAs, which matters when K is short: a tile of K = 1152 is 36 MMAs.
+//
+// Roles (448 threads per CTA): warp 0 producer, warp 1 MMA issuer (even CTA),
+// warps 2-5 scale-factor writers (a stage's scale chunks from shared memory to
+// the ring slot of its k-slice), warps 6-13 epilogue (two per TMEM lane
+// quarter, 32-column chunks in turn).
+//
+// Barriers (every wait bounded; cluster signals as in gemm2sm.cu):
+//   full[s]       in the leader: both CTAs' operand bytes of stage s
+//   sfs_full[s]   in each CTA: its scale chunks of stage s
+//   empty[s]      in each CTA: the stage's MMAs are done (multicast commit)
+//   sft_ready[k]  in the leader: ring slot k written by both CTAs' writers
+//   sft_free[k]   in each CTA: the slot's MMAs are done (multicast commit)
+//   acc_full[a]   in each CTA: accumulator a complete (multicast commit)
+//   acc_empty[a]  in the leader: drained by both CTAs' epilogue warps
+#include "gemm_pair.cuh"
+#include "linear.cuh"
+
+namespace mxmoe {
+namespace linear {
+
+constexpr int P_STAGES = 6;
+constexpr int P_SLOTS = 4;           // scale ring, k-slices
+constexpr int P_BN = 224;            // widest tile
+constexpr int P_EPI_WARPS = 8;
+constexpr int P_THREADS = 32 * (6 + P_EPI_WARPS);
+constexpr int P_SF_COL = 2 * P_BN;   // TMEM: two accumulators, then the ring
+constexpr int P_SLOT_COLS = 16;      // 4 (A) + BN / 32 (B)
+static_assert(P_SF_COL + P_SLOTS * P_SLOT_COLS <= TMEM_COLS, "tensor memory");
+
+constexpr int P_A_BYTES = BM * BK;
+constexpr int P_B_BYTES = P_BN / 2 * BK;
+constexpr int P_SF_BYTES = 4 * 512;  // A chunk, three 128-row chunks of B
+constexpr int P_OFF_B = P_STAGES * P_A_BYTES;
+constexpr int P_OFF_SF = P_OFF_B + P_STAGES * P_B_BYTES;
+constexpr int P_OFF_BAR = P_OFF_SF + P_STAGES * P_SF_BYTES;
+constexpr int P_NUM_BARS = 3 * P_STAGES + 2 * P_SLOTS + 4 + 1;
+constexpr int P_OFF_MISC = P_OFF_BAR + P_NUM_BARS * 8;
+constexpr int P_ALLOC = P_OFF_MISC + 16 + 1024;
+static_assert(P_B_BYTES % 1024 == 0 && P_ALLOC <= 232448, "shared memory");
+
+// 32 columns of one row: bias, activation, residual, rounding, store.
+// n: first column (a multiple of 32, < N); the second half may lie past N.
+__device__ __forceinline__ void finish_chunk(const LinParams& p, int64_t row, bool valid, int n,
+                                             const uint32_t (&v)[32], const uint32_t (&res)[16]) {
+  const bool hi = n + 16 < p.N;  // uniform
+  float a[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) a[i] = __uint_as_float(v[i]);
+  if (p.bias) {
+    if (p.bias32) {
+      const float4* b = reinterpret_cast<const float4*>(static_cast<const float*>(p.bias) + n);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < 4 || hi) {
+          const float4 w = __ldg(b + i);
+          a[4 * i] += w.x; a[4 * i + 1] += w.y; a[4 * i + 2] += w.z; a[4 * i + 3] += w.w;
+        }
+    } else {
+      const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + n);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < 2 || hi) {
+          const uint4 w = __ldg(b + i);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            a[8 * i + 2 * j] += bf16_bits_to_float(u[j] & 0xFFFFu);
+            a[8 * i + 2 * j + 1] += bf16_bits_to_float(u[j] >> 16);
+          }
+        }
+    }
+  }
+  activate_all(p.act, a);
+  if (p.out) {
+    uint32_t o[16];
+    if (p.res) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        a[2 * i] += bf16_bits_to_float(res[i] & 0xFFFFu);
+        a[2 * i + 1] += bf16_bits_to_float(res[i] >> 16);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = cvt_bf16x2(a[2 * i], a[2 * i + 1]);
+    if (!valid) return;
+    uint16_t* dst = p.out + row * p.N + n;
+    if (p.v32) {
+      st_v8(dst, *reinterpret_cast<const uint32_t(*)[8]>(&o[0]));
+      if (hi) st_v8(dst + 16, *reinterpret_cast<const uint32_t(*)[8]>(&o[8]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < 2 || hi) st_v4(dst + 8 * i, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+    }
+    return;
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < 16 || hi) m = umax(m, __float_as_uint(a[i]) & 0x7FFFFFFFu);
+  const uint32_t sb = e8m0_from_amax_bits(m);
+  const float inv = inv_scale_from_e8m0(sb);
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    o[i] = cvt_e4m3x4(a[4 * i] * inv, a[4 * i + 1] * inv, a[4 * i + 2] * inv, a[4 * i + 3] * inv);
+  if (!valid) return;
+  uint8_t* dst = p.oq + row * p.N + n;
+  st_v4(dst, make_uint4(o[0], o[1], o[2], o[3]));
+  if (hi) st_v4(dst + 16, make_uint4(o[4], o[5], o[6], o[7]));
+  const int KT = (p.N + 127) / 128, j = n >> 5;
+  p.os[tiled_scale_offset(row, j, KT)] = (uint8_t)sb;
+  if (n + 32 >= p.N)  // the row's last block: the slots after it hold 127
+    for (int jj = j + 1; jj < 4 * KT; ++jj) p.os[tiled_scale_offset(row, jj, KT)] = 127;
+}
+
+__global__ void __launch_bounds__(P_THREADS, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tmX,
+                       const __grid_constant__ CUtensorMap tmW, const LinParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~(uintptr_t)1023);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + P_OFF_MISC);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + P_OFF_MISC + 4);
+  const uint32_t bars = sbase + P_OFF_BAR;
+  auto bar_full = [&](int s) { return bars + 8u * s; };
+  auto bar_sfs = [&](int s) { return bars + 8u * (P_STAGES + s); };
+  auto bar_empty = [&](int s) { return bars + 8u * (2 * P_STAGES + s); };
+  auto bar_sft_ready = [&](int k) { return bars + 8u * (3 * P_STAGES + k); };
+  auto bar_sft_free = [&](int k) { return bars + 8u * (3 * P_STAGES + P_SLOTS + k); };
+  auto bar_acc_full = [&](int a) { return bars + 8u * (3 * P_STAGES + 2 * P_SLOTS + a); };
+  auto bar_acc_empty = [&](int a) { return bars + 8u * (3 * P_STAGES + 2 * P_SLOTS + 2 + a); };
+  const uint32_t bar_drain = bars + 8u * (3 * P_STAGES + 2 * P_SLOTS + 4);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P_STAGES; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_sfs(s), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int k = 0; k < P_SLOTS; ++k) {
+      mbar_init(bar_sft_ready(k), 2 * SF_WARPS);
+      mbar_init(bar_sft_free(k), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(bar_acc_full(a), 1);
+      mbar_init(bar_acc_empty(a), 2 * P_EPI_WARPS);
+    }
+    mbar_init(bar_drain, 1);
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(s_tmem)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialized before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int KT = (p.K + BK - 1) / BK;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  // tile -> this CTA's first row, the tile's first column
+  auto tile_at = [&](int tile, int64_t& row0, int& n0) {
+    const int mp = tile / p.tiles_n;
+    n0 = (tile - mp * p.tiles_n) * p.BN;
+    row0 = (int64_t)mp * (2 * BM) + (int64_t)rank * BM;
+  };
+
+  if (warp == 0) {
+    // ================= producer
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    uint32_t armed = 0, armed_parity = 0;  // this CTA's scale copies, for the abort drain
+    const uint32_t lead_full = mapa_cluster(bar_full(0), 0);
+    const uint32_t b_bytes = (uint32_t)(p.BN / 2 * BK);
+    const int64_t last_a = (p.M - 1) >> 7;
+    const int last_b = (p.N - 1) >> 7;
+    for (int tile = first; ok && tile < p.tiles; tile += step) {
+      int64_t row0;
+      int n0;
+      tile_at(tile, row0, n0);
+      const int64_t ra = min(row0 >> 7, last_a);
+      const int rb = n0 >> 7;
+      for (int kt = 0; kt < KT; ++kt) {
+        const bool got = wait_bar(bar_empty(stage), phase ^ 1, p.wait_limit, p.status, s_abort);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          if (leader) mbar_arrive_expect_tx(bar_full(stage), 2 * (P_A_BYTES + b_bytes));
+          const uint32_t fb = lead_full + 8u * stage;
+          tma_load_2d_pair(sbase + stage * P_A_BYTES, &tmX, kt * BK, (int)row0, fb);
+          tma_load_2d_pair(sbase + P_OFF_B + stage * P_B_BYTES, &tmW, kt * BK,
+                           n0 + (int)rank * (p.BN / 2), fb);
+          const uint32_t sf = sbase + P_OFF_SF + stage * P_SF_BYTES;
+          mbar_arrive_expect_tx(bar_sfs(stage), P_SF_BYTES);
+          bulk_copy_g2s(sf, p.sfx + (ra * KT + kt) * 512, 512, bar_sfs(stage));
+#pragma unroll
+          for (int c = 0; c < 3; ++c)
+            bulk_copy_g2s(sf + 512 * (c + 1), p.sfw + ((int64_t)min(rb + c, last_b) * KT + kt) * 512,
+                          512, bar_sfs(stage));
+        }
+        __syncwarp();
+        armed |= 1u << stage;
+        if (phase) armed_parity |= 1u << stage; else armed_parity &= ~(1u << stage);
+        if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
+      }
+    }
+    if (ok) {
+      // no commit of the pair is on its way to this CTA when it leaves
+      for (int i = 0; i < P_STAGES; ++i) {
+        wait_bar(bar_empty(stage), phase ^ 1, p.wait_limit, p.status, s_abort);
+        if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
+      }
+    } else {
+      volatile int no_abort = 0;
+      for (int s = 0; s < P_STAGES; ++s)
+        if ((armed >> s) & 1u)
+          wait_bar(bar_sfs(s), (armed_parity >> s) & 1u, 1ll << 32, nullptr, &no_abort);
+      // operand loads complete on the leader's barriers: a bounded moment to land
+      const long long t0 = clock64();
+      while (clock64() - t0 < 200000) __nanosleep(1000);
+    }
+  } else if (warp == 1) {
+    // ================= MMA issuer: one thread of the leader
+    if (leader && lane == 0) {
+      const uint32_t IDESC = make_idesc(2 * BM, p.BN);
+      int stage = 0;
+      uint32_t phase = 0, it = 0, n = 0;
+      bool ok = true, issued = false;
+      for (int tile = first; ok && tile < p.tiles; tile += step, ++n) {
+        const int a = n & 1;
+        if (!wait_bar_cluster(bar_acc_empty(a), ((n >> 1) & 1u) ^ 1u, p.wait_limit, p.status,
+                              s_abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int kt = 0; kt < KT; ++kt, ++it) {
+          const int k = it & (P_SLOTS - 1);
+          if (!wait_bar_cluster(bar_sft_ready(k), (it / P_SLOTS) & 1u, p.wait_limit, p.status,
+                                s_abort) ||
+              !wait_bar(bar_full(stage), phase, p.wait_limit, p.status, s_abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t adesc = make_sdesc(sbase + stage * P_A_BYTES, 16, 1024, 2);
+          const uint64_t bdesc = make_sdesc(sbase + P_OFF_B + stage * P_B_BYTES, 16, 1024, 2);
+          const uint32_t t_sf = tmem + P_SF_COL + k * P_SLOT_COLS;
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            tc2_mma_mxf8(tmem + a * P_BN, adesc + 2 * kk, bdesc + 2 * kk,
+                         IDESC | ((uint32_t)kk << 29) | ((uint32_t)kk << 4), t_sf, t_sf + 4,
+                         (kt | kk) != 0 ? 1u : 0u);
+          issued = true;
+          tc2_commit_both(bar_empty(stage));
+          tc2_commit_both(bar_sft_free(k));
+          if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        tc2_commit_both(bar_acc_full(a));
+      }
+      if (ok) {
+        // the last tiles' releases (some from the peer) land before exit
+        for (uint32_t i = n >= 2 ? n - 2 : 0; i < n; ++i)
+          wait_bar_cluster(bar_acc_empty(i & 1), (i >> 1) & 1u, p.wait_limit, p.status, s_abort);
+      } else if (issued) {
+        tc2_commit_both(bar_drain);
+        volatile int no_abort = 0;
+        wait_bar(bar_drain, 0, 1ll << 32, nullptr, &no_abort);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 6) {
+    // ================= scale-factor writers, one per TMEM lane quarter
+    const uint32_t t_q = tmem + ((uint32_t)((warp & 3) * 32) << 16) + P_SF_COL;
+    const uint32_t lead_ready = mapa_cluster(bar_sft_ready(0), 0);
+    int stage = 0;
+    uint32_t phase = 0, it = 0;
+    bool ok = true;
+    for (int tile = first; ok && tile < p.tiles; tile += step) {
+      int64_t row0;
+      int n0;
+      tile_at(tile, row0, n0);
+      const int g0 = (n0 >> 5) & 3;  // first 32-row group in its 128-row block
+      for (int kt = 0; kt < KT; ++kt, ++it) {
+        const int k = it & (P_SLOTS - 1);
+        const bool got =
+            wait_bar(bar_sfs(stage), phase, p.wait_limit, p.status, s_abort) &&
+            wait_bar(bar_sft_free(k), ((it / P_SLOTS) & 1u) ^ 1u, p.wait_limit, p.status, s_abort);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* sf = smem + P_OFF_SF + stage * P_SF_BYTES + lane * 16;
+        const uint32_t col = t_q + k * P_SLOT_COLS;
+        tmem_st_4(col, *reinterpret_cast<const uint4*>(sf));
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {  // group g0 + j: chunk (g0 + j) / 4, word (g0 + j) % 4
+          const int g = g0 + j;
+          w[j] = *reinterpret_cast<const uint32_t*>(sf + 512 * (1 + (g >> 2)) + 4 * (g & 3));
+        }
+        tmem_st_4(col + 4, make_uint4(w[0], w[1], w[2], w[3]));
+        tmem_st_4(col + 8, make_uint4(w[4], w[5], w[6], w[7]));
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(bar_sft_ready(k));
+          else mbar_arrive_cluster(lead_ready + 8u * k);
+        }
+        if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
+      }
+    }
+    // the commits that free the last slots have landed
+    if (ok)
+      for (uint32_t i = it >= P_SLOTS ? it - P_SLOTS : 0; i < it; ++i)
+        wait_bar(bar_sft_free(i & (P_SLOTS - 1)), (i / P_SLOTS) & 1u, p.wait_limit, p.status,
+                 s_abort);
+    __syncwarp();
+  } else {
+    // ================= epilogue
+    const int q = warp & 3, half = (warp - 6) >> 2;
+    const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16);
+    const uint32_t lead_acc_empty = mapa_cluster(bar_acc_empty(0), 0);
+    const int nch = p.BN / 32;
+    uint32_t n = 0;
+    for (int tile = first; tile < p.tiles; tile += step, ++n) {
+      const int a = n & 1;
+      int64_t row0;
+      int n0;
+      tile_at(tile, row0, n0);
+      const int64_t row = row0 + q * 32 + lane;
+      const bool valid = row < p.M;
+      const bool got = wait_bar(bar_acc_full(a), (n >> 1) & 1u, p.wait_limit, p.status, s_abort);
+      if (!__all_sync(0xffffffffu, got)) break;
+      tc_fence_after();
+      for (int c = half; c < nch; c += 2) {
+        const int col = n0 + 32 * c;
+        uint32_t v[32], res[16];
+        tmem_ld_32(t_row + a * P_BN + 32 * c, v);
+        if (p.res && valid && col < p.N) {
+          const uint16_t* src = p.res + row * p.N + col;
+          const bool hi = col + 16 < p.N;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < 2 || hi) {
+              const uint4 u = *reinterpret_cast<const uint4*>(src + 8 * i);
+              res[4 * i] = u.x; res[4 * i + 1] = u.y; res[4 * i + 2] = u.z; res[4 * i + 3] = u.w;
+            }
+        }
+        tmem_ld_wait();
+        if (c + 2 >= nch) {  // this warp's last read of the accumulator
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader) mbar_arrive(bar_acc_empty(a));
+            else mbar_arrive_cluster(lead_acc_empty + 8u * a);
+          }
+        }
+        if (col < p.N) finish_chunk(p, row, valid, col, v, res);  // warp-uniform
+      }
+    }
+  }
+
+  // ---- teardown
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may still signal it
+  tc_fence_after();
+  if (warp == 1) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// Cycles of one MMA by tile width: the shared-memory bound above.
+static double mma_cycles(int bn) { return (384 + 1.5 * bn) * 32 / 128; }
+
+double pair_cycles(int64_t M, int N, int K, int* bn) {
+  const int64_t pairs = std::max(1, num_sms() / 2);
+  double best = 0;
+  for (int b : {224, 192, 128}) {
+    const int64_t tiles = ceil_div(M, 2 * BM) * ceil_div(N, b);
+    const double t = (double)ceil_div(tiles, pairs) * (double)ceil_div(K, BK) * 4 * mma_cycles(b);
+    if (best == 0 || t < best) {
+      best = t;
+      *bn = b;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_pair(const uint8_t* xq, const uint8_t* wq, LinParams p, cudaStream_t stream) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  static int max_clusters[64];
+  static uint64_t configured[64] = {0};  // context id the attribute was set in
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(P_THREADS);
+  cfg.dynamicSmemBytes = P_ALLOC;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const uint64_t ctx = context_id();
+  if (ctx == 0 || configured[dev] != ctx) {
+    const cudaError_t err = cudaFuncSetAttribute(
+        linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P_ALLOC);
+    if (err != cudaSuccess) return err;
+    cfg.gridDim = dim3(2 * 64);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    max_clusters[dev] = n;
+    configured[dev] = context_id();
+  }
+  if (max_clusters[dev] <= 0) return cudaErrorNotSupported;
+  p.tiles_n = (int)ceil_div(p.N, p.BN);
+  const int64_t tiles = ceil_div(p.M, 2 * BM) * p.tiles_n;
+  if (tiles >= (1ll << 31)) return cudaErrorNotSupported;
+  p.tiles = (int)tiles;
+  p.v32 = (((uintptr_t)p.out | (uintptr_t)p.res) & 31u) == 0;
+  CUtensorMap tmX, tmW;
+  if (!make_map(&tmX, xq, (uint64_t)p.K, (uint64_t)p.M, BK, BM) ||
+      !make_map(&tmW, wq, (uint64_t)p.K, (uint64_t)p.N, BK, (uint32_t)(p.BN / 2)))
+    return cudaErrorInvalidValue;
+  const int clusters = (int)std::min<int64_t>(
+      {tiles, (int64_t)max_clusters[dev], (int64_t)std::max(1, num_sms() / 2)});
+  cfg.gridDim = dim3(2 * clusters);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, linear_pair_kernel, tmX, tmW, p);
+}
+
+}  // namespace linear
+}  // namespace mxmoe
