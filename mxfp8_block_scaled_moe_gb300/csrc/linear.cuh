@@ -58,6 +58,17 @@ __device__ __forceinline__ void activate_all(int act, float (&v)[N]) {
   }
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // CTA pairs (linear_pair.cu).  cudaErrorNotSupported: the device cannot
 // co-schedule pairs.
 cudaError_t launch_pair(const uint8_t* xq, const uint8_t* wq, LinParams p, cudaStream_t stream);

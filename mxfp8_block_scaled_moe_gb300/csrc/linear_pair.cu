@@ -16,17 +16,19 @@
 // epilogue of a tile (bias, activation, residual, stores) runs under the next
 // tile's MMAs, which matters when K is short: a tile of K = 1152 is 36 MMAs.
 //
-// Roles (448 threads per CTA): warp 0 producer, warp 1 MMA issuer (even CTA),
+// Roles (480 threads per CTA): warp 0 producer, warp 1 MMA issuer (even CTA),
 // warps 2-5 scale-factor writers (a stage's scale chunks from shared memory to
 // the ring slot of its k-slice), warps 6-13 epilogue (two per TMEM lane
-// quarter, 32-column chunks in turn).
+// quarter, 32-column chunks in turn), warp 14 scale producer (bulk copies of
+// the scale chunks; on warp 0 their issue slowed the operand loads).
 //
 // Barriers (every wait bounded; cluster signals as in gemm2sm.cu):
 //   full[s]       in the leader: both CTAs' operand bytes of stage s
 //   sfs_full[s]   in each CTA: its scale chunks of stage s
-//   empty[s]      in each CTA: the stage's MMAs are done (multicast commit)
+//   empty[s]      in each CTA: the stage's MMAs are done (multicast commit);
+//                 the scale writers wait on it too: a slice's ring slot is free
+//                 when the MMAs of the slice four before it are done
 //   sft_ready[k]  in the leader: ring slot k written by both CTAs' writers
-//   sft_free[k]   in each CTA: the slot's MMAs are done (multicast commit)
 //   acc_full[a]   in each CTA: accumulator a complete (multicast commit)
 //   acc_empty[a]  in the leader: drained by both CTAs' epilogue warps
 #include "gemm_pair.cuh"
@@ -39,18 +41,19 @@ constexpr int P_STAGES = 6;
 constexpr int P_SLOTS = 4;           // scale ring, k-slices
 constexpr int P_BN = 224;            // widest tile
 constexpr int P_EPI_WARPS = 8;
-constexpr int P_THREADS = 32 * (6 + P_EPI_WARPS);
+constexpr int P_SF_WARP = 6 + P_EPI_WARPS;  // scale producer
+constexpr int P_THREADS = 32 * (P_SF_WARP + 1);
 constexpr int P_SF_COL = 2 * P_BN;   // TMEM: two accumulators, then the ring
 constexpr int P_SLOT_COLS = 16;      // 4 (A) + BN / 32 (B)
 static_assert(P_SF_COL + P_SLOTS * P_SLOT_COLS <= TMEM_COLS, "tensor memory");
 
 constexpr int P_A_BYTES = BM * BK;
 constexpr int P_B_BYTES = P_BN / 2 * BK;
-constexpr int P_SF_BYTES = 4 * 512;  // A chunk, three 128-row chunks of B
 constexpr int P_OFF_B = P_STAGES * P_A_BYTES;
+constexpr int P_SF_BYTES = 4 * 512;  // per stage: A chunk, three 128-row chunks of B
 constexpr int P_OFF_SF = P_OFF_B + P_STAGES * P_B_BYTES;
 constexpr int P_OFF_BAR = P_OFF_SF + P_STAGES * P_SF_BYTES;
-constexpr int P_NUM_BARS = 3 * P_STAGES + 2 * P_SLOTS + 4 + 1;
+constexpr int P_NUM_BARS = 3 * P_STAGES + P_SLOTS + 4 + 1;
 constexpr int P_OFF_MISC = P_OFF_BAR + P_NUM_BARS * 8;
 constexpr int P_ALLOC = P_OFF_MISC + 16 + 1024;
 static_assert(P_B_BYTES % 1024 == 0 && P_ALLOC <= 232448, "shared memory");
@@ -138,30 +141,29 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the shuffle tells the compiler that the warp index is uniform)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + P_OFF_MISC);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + P_OFF_MISC + 4);
   const uint32_t bars = sbase + P_OFF_BAR;
   auto bar_full = [&](int s) { return bars + 8u * s; };
-  auto bar_sfs = [&](int s) { return bars + 8u * (P_STAGES + s); };
-  auto bar_empty = [&](int s) { return bars + 8u * (2 * P_STAGES + s); };
-  auto bar_sft_ready = [&](int k) { return bars + 8u * (3 * P_STAGES + k); };
-  auto bar_sft_free = [&](int k) { return bars + 8u * (3 * P_STAGES + P_SLOTS + k); };
-  auto bar_acc_full = [&](int a) { return bars + 8u * (3 * P_STAGES + 2 * P_SLOTS + a); };
-  auto bar_acc_empty = [&](int a) { return bars + 8u * (3 * P_STAGES + 2 * P_SLOTS + 2 + a); };
-  const uint32_t bar_drain = bars + 8u * (3 * P_STAGES + 2 * P_SLOTS + 4);
+  auto bar_empty = [&](int s) { return bars + 8u * (P_STAGES + s); };
+  auto bar_sft_ready = [&](int k) { return bars + 8u * (2 * P_STAGES + k); };
+  auto bar_acc_full = [&](int a) { return bars + 8u * (2 * P_STAGES + P_SLOTS + a); };
+  auto bar_acc_empty = [&](int a) { return bars + 8u * (2 * P_STAGES + P_SLOTS + 2 + a); };
+  const uint32_t bar_drain = bars + 8u * (2 * P_STAGES + P_SLOTS + 4);
+  auto bar_sfs = [&](int s) { return bars + 8u * (2 * P_STAGES + P_SLOTS + 5 + s); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < P_STAGES; ++s) {
       mbar_init(bar_full(s), 1);
-      mbar_init(bar_sfs(s), 1);
       mbar_init(bar_empty(s), 1);
+      mbar_init(bar_sfs(s), 1);
     }
     for (int k = 0; k < P_SLOTS; ++k) {
       mbar_init(bar_sft_ready(k), 2 * SF_WARPS);
-      mbar_init(bar_sft_free(k), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(bar_acc_full(a), 1);
@@ -196,44 +198,30 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   };
 
   if (warp == 0) {
-    // ================= producer
+    // ================= producer (one elected thread issues, as below)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    uint32_t armed = 0, armed_parity = 0;  // this CTA's scale copies, for the abort drain
     const uint32_t lead_full = mapa_cluster(bar_full(0), 0);
     const uint32_t b_bytes = (uint32_t)(p.BN / 2 * BK);
-    const int64_t last_a = (p.M - 1) >> 7;
-    const int last_b = (p.N - 1) >> 7;
     for (int tile = first; ok && tile < p.tiles; tile += step) {
       int64_t row0;
       int n0;
       tile_at(tile, row0, n0);
-      const int64_t ra = min(row0 >> 7, last_a);
-      const int rb = n0 >> 7;
+      const int b_row = n0 + (int)rank * (p.BN / 2);
       for (int kt = 0; kt < KT; ++kt) {
         const bool got = wait_bar(bar_empty(stage), phase ^ 1, p.wait_limit, p.status, s_abort);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
-        if (lane == 0) {
+        if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(bar_full(stage), 2 * (P_A_BYTES + b_bytes));
           const uint32_t fb = lead_full + 8u * stage;
           tma_load_2d_pair(sbase + stage * P_A_BYTES, &tmX, kt * BK, (int)row0, fb);
-          tma_load_2d_pair(sbase + P_OFF_B + stage * P_B_BYTES, &tmW, kt * BK,
-                           n0 + (int)rank * (p.BN / 2), fb);
-          const uint32_t sf = sbase + P_OFF_SF + stage * P_SF_BYTES;
-          mbar_arrive_expect_tx(bar_sfs(stage), P_SF_BYTES);
-          bulk_copy_g2s(sf, p.sfx + (ra * KT + kt) * 512, 512, bar_sfs(stage));
-#pragma unroll
-          for (int c = 0; c < 3; ++c)
-            bulk_copy_g2s(sf + 512 * (c + 1), p.sfw + ((int64_t)min(rb + c, last_b) * KT + kt) * 512,
-                          512, bar_sfs(stage));
+          tma_load_2d_pair(sbase + P_OFF_B + stage * P_B_BYTES, &tmW, kt * BK, b_row, fb);
         }
         __syncwarp();
-        armed |= 1u << stage;
-        if (phase) armed_parity |= 1u << stage; else armed_parity &= ~(1u << stage);
         if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
       }
     }
@@ -244,34 +232,34 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
       }
     } else {
-      volatile int no_abort = 0;
-      for (int s = 0; s < P_STAGES; ++s)
-        if ((armed >> s) & 1u)
-          wait_bar(bar_sfs(s), (armed_parity >> s) & 1u, 1ll << 32, nullptr, &no_abort);
-      // operand loads complete on the leader's barriers: a bounded moment to land
+      // abort: operand loads complete on the leader's barriers: a bounded moment to land
       const long long t0 = clock64();
       while (clock64() - t0 < 200000) __nanosleep(1000);
     }
   } else if (warp == 1) {
-    // ================= MMA issuer: one thread of the leader
-    if (leader && lane == 0) {
+    // ================= MMA issuer.  The leader's whole warp walks the loop and
+    // one elected thread issues: the descriptors, computed by a converged
+    // warp, stay in uniform registers, where the instruction wants them.
+    if (leader) {
       const uint32_t IDESC = make_idesc(2 * BM, p.BN);
       int stage = 0;
       uint32_t phase = 0, it = 0, n = 0;
       bool ok = true, issued = false;
       for (int tile = first; ok && tile < p.tiles; tile += step, ++n) {
         const int a = n & 1;
-        if (!wait_bar_cluster(bar_acc_empty(a), ((n >> 1) & 1u) ^ 1u, p.wait_limit, p.status,
-                              s_abort)) {
+        const bool got = wait_bar_cluster(bar_acc_empty(a), ((n >> 1) & 1u) ^ 1u, p.wait_limit,
+                                          p.status, s_abort);
+        if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
         tc_fence_after();
         for (int kt = 0; kt < KT; ++kt, ++it) {
           const int k = it & (P_SLOTS - 1);
-          if (!wait_bar_cluster(bar_sft_ready(k), (it / P_SLOTS) & 1u, p.wait_limit, p.status,
-                                s_abort) ||
-              !wait_bar(bar_full(stage), phase, p.wait_limit, p.status, s_abort)) {
+          const bool got_k = wait_bar_cluster(bar_sft_ready(k), (it / P_SLOTS) & 1u, p.wait_limit,
+                                              p.status, s_abort) &&
+                             wait_bar(bar_full(stage), phase, p.wait_limit, p.status, s_abort);
+          if (!__all_sync(0xffffffffu, got_k)) {
             ok = false;
             break;
           }
@@ -279,47 +267,55 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           const uint64_t adesc = make_sdesc(sbase + stage * P_A_BYTES, 16, 1024, 2);
           const uint64_t bdesc = make_sdesc(sbase + P_OFF_B + stage * P_B_BYTES, 16, 1024, 2);
           const uint32_t t_sf = tmem + P_SF_COL + k * P_SLOT_COLS;
+          const uint32_t t_acc = tmem + a * P_BN;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            tc2_mma_mxf8(tmem + a * P_BN, adesc + 2 * kk, bdesc + 2 * kk,
-                         IDESC | ((uint32_t)kk << 29) | ((uint32_t)kk << 4), t_sf, t_sf + 4,
-                         (kt | kk) != 0 ? 1u : 0u);
+            for (int kk = 0; kk < BK / 32; ++kk)
+              tc2_mma_mxf8(t_acc, adesc + 2 * kk, bdesc + 2 * kk,
+                           IDESC | ((uint32_t)kk << 29) | ((uint32_t)kk << 4), t_sf, t_sf + 4,
+                           (kt | kk) != 0 ? 1u : 0u);
+            tc2_commit_both(bar_empty(stage));
+            if (kt == KT - 1) tc2_commit_both(bar_acc_full(a));
+          }
+          __syncwarp();
           issued = true;
-          tc2_commit_both(bar_empty(stage));
-          tc2_commit_both(bar_sft_free(k));
           if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
         }
-        if (!ok) break;
-        tc2_commit_both(bar_acc_full(a));
       }
       if (ok) {
         // the last tiles' releases (some from the peer) land before exit
         for (uint32_t i = n >= 2 ? n - 2 : 0; i < n; ++i)
           wait_bar_cluster(bar_acc_empty(i & 1), (i >> 1) & 1u, p.wait_limit, p.status, s_abort);
       } else if (issued) {
-        tc2_commit_both(bar_drain);
+        if (elect_one()) tc2_commit_both(bar_drain);
+        __syncwarp();
         volatile int no_abort = 0;
         wait_bar(bar_drain, 0, 1ll << 32, nullptr, &no_abort);
       }
     }
     __syncwarp();
   } else if (warp < 6) {
-    // ================= scale-factor writers, one per TMEM lane quarter
+    // ================= scale-factor writers, one per TMEM lane quarter (each
+    // quarter holds every chunk).  A lane's 16 bytes of a chunk are its four
+    // 32-row groups' words; a tile's B groups start at word g0 of its first
+    // 128-row block and span up to three blocks.
     const uint32_t t_q = tmem + ((uint32_t)((warp & 3) * 32) << 16) + P_SF_COL;
     const uint32_t lead_ready = mapa_cluster(bar_sft_ready(0), 0);
-    int stage = 0;
-    uint32_t phase = 0, it = 0;
+    int stage = 0, e_stage = 0;  // e: stage and parity of the slice P_SLOTS before
+    uint32_t phase = 0, e_phase = 0, it = 0;
     bool ok = true;
     for (int tile = first; ok && tile < p.tiles; tile += step) {
       int64_t row0;
       int n0;
       tile_at(tile, row0, n0);
-      const int g0 = (n0 >> 5) & 3;  // first 32-row group in its 128-row block
+      const int g0 = (n0 >> 5) & 3;
       for (int kt = 0; kt < KT; ++kt, ++it) {
         const int k = it & (P_SLOTS - 1);
-        const bool got =
-            wait_bar(bar_sfs(stage), phase, p.wait_limit, p.status, s_abort) &&
-            wait_bar(bar_sft_free(k), ((it / P_SLOTS) & 1u) ^ 1u, p.wait_limit, p.status, s_abort);
+        bool got = wait_bar(bar_sfs(stage), phase, p.wait_limit, p.status, s_abort);
+        if (it >= P_SLOTS) {
+          got = got && wait_bar(bar_empty(e_stage), e_phase, p.wait_limit, p.status, s_abort);
+          if (++e_stage == P_STAGES) { e_stage = 0; e_phase ^= 1; }
+        }
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
@@ -345,11 +341,47 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
       }
     }
-    // the commits that free the last slots have landed
-    if (ok)
-      for (uint32_t i = it >= P_SLOTS ? it - P_SLOTS : 0; i < it; ++i)
-        wait_bar(bar_sft_free(i & (P_SLOTS - 1)), (i / P_SLOTS) & 1u, p.wait_limit, p.status,
-                 s_abort);
+    __syncwarp();
+  } else if (warp == P_SF_WARP) {
+    // ================= scale producer
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    bool ok = true;
+    const int64_t last_a = (p.M - 1) >> 7;
+    const int last_b = (p.N - 1) >> 7;
+    for (int tile = first; ok && tile < p.tiles; tile += step) {
+      int64_t row0;
+      int n0;
+      tile_at(tile, row0, n0);
+      const uint8_t* at_a = p.sfx + min(row0 >> 7, last_a) * KT * 512;
+      const int rb = n0 >> 7;
+      for (int kt = 0; kt < KT; ++kt) {
+        const bool got = wait_bar(bar_empty(stage), phase ^ 1, p.wait_limit, p.status, s_abort);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t sf = sbase + P_OFF_SF + stage * P_SF_BYTES;
+          mbar_arrive_expect_tx(bar_sfs(stage), P_SF_BYTES);
+          bulk_copy_g2s(sf, at_a + (int64_t)kt * 512, 512, bar_sfs(stage));
+#pragma unroll
+          for (int c = 0; c < 3; ++c)  // (blocks past the last one: copied again, not used)
+            bulk_copy_g2s(sf + 512 * (c + 1), p.sfw + ((int64_t)min(rb + c, last_b) * KT + kt) * 512,
+                          512, bar_sfs(stage));
+        }
+        __syncwarp();
+        armed |= 1u << stage;
+        if (phase) armed_parity |= 1u << stage; else armed_parity &= ~(1u << stage);
+        if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
+      }
+    }
+    if (!ok) {  // abort: this CTA's copies land before it leaves
+      volatile int no_abort = 0;
+      for (int s = 0; s < P_STAGES; ++s)
+        if ((armed >> s) & 1u)
+          wait_bar(bar_sfs(s), (armed_parity >> s) & 1u, 1ll << 32, nullptr, &no_abort);
+    }
     __syncwarp();
   } else {
     // ================= epilogue
