@@ -381,8 +381,9 @@ cudaError_t launch_linear_fused(const uint8_t* xq, const uint8_t* xs, const uint
   p.status = device_status_ptr();
   p.wait_limit = wait_limit_cycles();
   if (M > 256) {
-    pair_cycles(M, N, K, &p.BN);
-    const cudaError_t err = launch_pair(xq, wq, p, stream);
+    int bn = 0;
+    pair_cycles(M, N, K, &bn);
+    const cudaError_t err = launch_pair(xq, wq, p, bn, stream);
     if (err != cudaErrorNotSupported) return err;
   }
   const Plan pl = make_plan(M, N, K);

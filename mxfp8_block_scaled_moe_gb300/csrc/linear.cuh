@@ -21,7 +21,7 @@ struct LinParams {
   int N, K, act;
   bool bias32;
   int NT, stages, nsplit;  // split kernel: token tile, pipeline stages, K ranges
-  int BN, tiles_n, tiles;  // pair kernel: columns per tile, n-tiles, tiles
+  int tiles_n, tiles;      // pair kernel: n-tiles, tiles
   bool v32;                // pair kernel: out / residual rows are 32-byte aligned
   int* status;
   long long wait_limit;
@@ -69,9 +69,23 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
+// Whether the phase is over, without waiting for it.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // CTA pairs (linear_pair.cu).  cudaErrorNotSupported: the device cannot
 // co-schedule pairs.
-cudaError_t launch_pair(const uint8_t* xq, const uint8_t* wq, LinParams p, cudaStream_t stream);
+cudaError_t launch_pair(const uint8_t* xq, const uint8_t* wq, const LinParams& p, int bn,
+                        cudaStream_t stream);
 // Estimated SM cycles of the pair kernel on this product, and the tile width
 // it would take.
 double pair_cycles(int64_t M, int N, int K, int* bn);

@@ -17,18 +17,19 @@
 // tile's MMAs, which matters when K is short: a tile of K = 1152 is 36 MMAs.
 //
 // Roles (480 threads per CTA): warp 0 producer, warp 1 MMA issuer (even CTA),
-// warps 2-5 scale-factor writers (a stage's scale chunks from shared memory to
-// the ring slot of its k-slice), warps 6-13 epilogue (two per TMEM lane
+// warps 2-5 scale-factor writers, warps 6-13 epilogue (two per TMEM lane
 // quarter, 32-column chunks in turn), warp 14 scale producer (bulk copies of
-// the scale chunks; on warp 0 their issue slowed the operand loads).
+// the scale chunks; on warp 0 their issue slowed the operand loads).  The
+// scales move in segments of two k-slices: a writer's waits, reads, stores and
+// arrival take about 550 cycles however much they move, more than a slice's MMAs.
 //
 // Barriers (every wait bounded; cluster signals as in gemm2sm.cu):
 //   full[s]       in the leader: both CTAs' operand bytes of stage s
-//   sfs_full[s]   in each CTA: its scale chunks of stage s
-//   empty[s]      in each CTA: the stage's MMAs are done (multicast commit);
-//                 the scale writers wait on it too: a slice's ring slot is free
-//                 when the MMAs of the slice four before it are done
-//   sft_ready[k]  in the leader: ring slot k written by both CTAs' writers
+//   empty[s]      in each CTA: the stage's MMAs are done (multicast commit)
+//   sfs_full[b]   in each CTA: its scale chunks of staged segment b
+//   sfs_free[b]   in each CTA: read by the scale writers
+//   sft_ready[g]  in the leader: tensor-memory segment g written by both CTAs
+//   sft_free[g]   in each CTA: the segment's MMAs are done (multicast commit)
 //   acc_full[a]   in each CTA: accumulator a complete (multicast commit)
 //   acc_empty[a]  in the leader: drained by both CTAs' epilogue warps
 #include "gemm_pair.cuh"
@@ -37,26 +38,36 @@
 namespace mxmoe {
 namespace linear {
 
-constexpr int P_STAGES = 6;
-constexpr int P_SLOTS = 4;           // scale ring, k-slices
-constexpr int P_BN = 224;            // widest tile
 constexpr int P_EPI_WARPS = 8;
 constexpr int P_SF_WARP = 6 + P_EPI_WARPS;  // scale producer
 constexpr int P_THREADS = 32 * (P_SF_WARP + 1);
-constexpr int P_SF_COL = 2 * P_BN;   // TMEM: two accumulators, then the ring
-constexpr int P_SLOT_COLS = 16;      // 4 (A) + BN / 32 (B)
-static_assert(P_SF_COL + P_SLOTS * P_SLOT_COLS <= TMEM_COLS, "tensor memory");
-
 constexpr int P_A_BYTES = BM * BK;
-constexpr int P_B_BYTES = P_BN / 2 * BK;
-constexpr int P_OFF_B = P_STAGES * P_A_BYTES;
-constexpr int P_SF_BYTES = 4 * 512;  // per stage: A chunk, three 128-row chunks of B
-constexpr int P_OFF_SF = P_OFF_B + P_STAGES * P_B_BYTES;
-constexpr int P_OFF_BAR = P_OFF_SF + P_STAGES * P_SF_BYTES;
-constexpr int P_NUM_BARS = 3 * P_STAGES + P_SLOTS + 4 + 1;
-constexpr int P_OFF_MISC = P_OFF_BAR + P_NUM_BARS * 8;
-constexpr int P_ALLOC = P_OFF_MISC + 16 + 1024;
-static_assert(P_B_BYTES % 1024 == 0 && P_ALLOC <= 232448, "shared memory");
+constexpr int P_SEG = 2;                    // k-slices per scale segment
+constexpr int P_SFS = 4;                    // scale segments staged in shared memory
+constexpr int P_SF_BYTES = 4 * P_SEG * 512; // per segment: A chunks, three 128-row blocks of B
+
+// What a tile width leaves room for: pipeline stages in shared memory, scale
+// segments in tensor memory beside the two accumulators, each slice 4 (A) +
+// BN / 32 (B) columns rounded up to 4.
+template <int BN>
+struct Pair {
+  static constexpr int B_BYTES = BN / 2 * BK;
+  static constexpr int STAGES = BN == 224 ? 6 : BN == 192 ? 7 : 8;
+  static constexpr int SLICE_COLS = (4 + BN / 32 + 3) / 4 * 4;
+  static constexpr int SEG_COLS = P_SEG * SLICE_COLS;
+  static constexpr int SF_COL = 2 * BN;
+  static constexpr int SEGS = (TMEM_COLS - SF_COL) / SEG_COLS >= 4 ? 4 : 2;
+  static constexpr int OFF_B = STAGES * P_A_BYTES;
+  static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
+  static constexpr int OFF_BAR = OFF_SF + P_SFS * P_SF_BYTES;
+  // full, empty [STAGES], sfs_full, sfs_free [P_SFS], sft_ready, sft_free [SEGS],
+  // acc_full, acc_empty [2], drain
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * P_SFS + 2 * SEGS + 5;
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int ALLOC = OFF_MISC + 16 + 1024;
+  static_assert(SF_COL + SEGS * SEG_COLS <= TMEM_COLS, "tensor memory");
+  static_assert(B_BYTES % 1024 == 0 && ALLOC <= 232448, "shared memory");
+};
 
 // 32 columns of one row: bias, activation, residual, rounding, store.
 // n: first column (a multiple of 32, < N); the second half may lie past N.
@@ -134,9 +145,12 @@ __device__ __forceinline__ void finish_chunk(const LinParams& p, int64_t row, bo
     for (int jj = j + 1; jj < 4 * KT; ++jj) p.os[tiled_scale_offset(row, jj, KT)] = 127;
 }
 
+template <int BN>
 __global__ void __launch_bounds__(P_THREADS, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmW, const LinParams p) {
+  using L = Pair<BN>;
+  constexpr int STAGES = L::STAGES, SEGS = L::SEGS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
@@ -145,25 +159,33 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + P_OFF_MISC);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + P_OFF_MISC + 4);
-  const uint32_t bars = sbase + P_OFF_BAR;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  const uint32_t bars = sbase + L::OFF_BAR;
   auto bar_full = [&](int s) { return bars + 8u * s; };
-  auto bar_empty = [&](int s) { return bars + 8u * (P_STAGES + s); };
-  auto bar_sft_ready = [&](int k) { return bars + 8u * (2 * P_STAGES + k); };
-  auto bar_acc_full = [&](int a) { return bars + 8u * (2 * P_STAGES + P_SLOTS + a); };
-  auto bar_acc_empty = [&](int a) { return bars + 8u * (2 * P_STAGES + P_SLOTS + 2 + a); };
-  const uint32_t bar_drain = bars + 8u * (2 * P_STAGES + P_SLOTS + 4);
-  auto bar_sfs = [&](int s) { return bars + 8u * (2 * P_STAGES + P_SLOTS + 5 + s); };
+  auto bar_empty = [&](int s) { return bars + 8u * (STAGES + s); };
+  const uint32_t bars2 = bars + 8u * (2 * STAGES);
+  auto bar_sfs_full = [&](int b) { return bars2 + 8u * b; };
+  auto bar_sfs_free = [&](int b) { return bars2 + 8u * (P_SFS + b); };
+  auto bar_sft_ready = [&](int g) { return bars2 + 8u * (2 * P_SFS + g); };
+  auto bar_sft_free = [&](int g) { return bars2 + 8u * (2 * P_SFS + SEGS + g); };
+  const uint32_t bars3 = bars2 + 8u * (2 * P_SFS + 2 * SEGS);
+  auto bar_acc_full = [&](int a) { return bars3 + 8u * a; };
+  auto bar_acc_empty = [&](int a) { return bars3 + 8u * (2 + a); };
+  const uint32_t bar_drain = bars3 + 32u;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < P_STAGES; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full(s), 1);
       mbar_init(bar_empty(s), 1);
-      mbar_init(bar_sfs(s), 1);
     }
-    for (int k = 0; k < P_SLOTS; ++k) {
-      mbar_init(bar_sft_ready(k), 2 * SF_WARPS);
+    for (int b = 0; b < P_SFS; ++b) {
+      mbar_init(bar_sfs_full(b), 1);
+      mbar_init(bar_sfs_free(b), SF_WARPS);
+    }
+    for (int g = 0; g < SEGS; ++g) {
+      mbar_init(bar_sft_ready(g), 2 * SF_WARPS);
+      mbar_init(bar_sft_free(g), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(bar_acc_full(a), 1);
@@ -193,7 +215,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   // tile -> this CTA's first row, the tile's first column
   auto tile_at = [&](int tile, int64_t& row0, int& n0) {
     const int mp = tile / p.tiles_n;
-    n0 = (tile - mp * p.tiles_n) * p.BN;
+    n0 = (tile - mp * p.tiles_n) * BN;
     row0 = (int64_t)mp * (2 * BM) + (int64_t)rank * BM;
   };
 
@@ -203,12 +225,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     uint32_t phase = 0;
     bool ok = true;
     const uint32_t lead_full = mapa_cluster(bar_full(0), 0);
-    const uint32_t b_bytes = (uint32_t)(p.BN / 2 * BK);
     for (int tile = first; ok && tile < p.tiles; tile += step) {
       int64_t row0;
       int n0;
       tile_at(tile, row0, n0);
-      const int b_row = n0 + (int)rank * (p.BN / 2);
+      const int b_row = n0 + (int)rank * (BN / 2);
       for (int kt = 0; kt < KT; ++kt) {
         const bool got = wait_bar(bar_empty(stage), phase ^ 1, p.wait_limit, p.status, s_abort);
         if (!__all_sync(0xffffffffu, got)) {
@@ -216,20 +237,20 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           break;
         }
         if (elect_one()) {
-          if (leader) mbar_arrive_expect_tx(bar_full(stage), 2 * (P_A_BYTES + b_bytes));
+          if (leader) mbar_arrive_expect_tx(bar_full(stage), 2 * (P_A_BYTES + L::B_BYTES));
           const uint32_t fb = lead_full + 8u * stage;
           tma_load_2d_pair(sbase + stage * P_A_BYTES, &tmX, kt * BK, (int)row0, fb);
-          tma_load_2d_pair(sbase + P_OFF_B + stage * P_B_BYTES, &tmW, kt * BK, b_row, fb);
+          tma_load_2d_pair(sbase + L::OFF_B + stage * L::B_BYTES, &tmW, kt * BK, b_row, fb);
         }
         __syncwarp();
-        if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
       }
     }
     if (ok) {
       // no commit of the pair is on its way to this CTA when it leaves
-      for (int i = 0; i < P_STAGES; ++i) {
+      for (int i = 0; i < STAGES; ++i) {
         wait_bar(bar_empty(stage), phase ^ 1, p.wait_limit, p.status, s_abort);
-        if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
       }
     } else {
       // abort: operand loads complete on the leader's barriers: a bounded moment to land
@@ -241,10 +262,10 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     // one elected thread issues: the descriptors, computed by a converged
     // warp, stay in uniform registers, where the instruction wants them.
     if (leader) {
-      const uint32_t IDESC = make_idesc(2 * BM, p.BN);
-      int stage = 0;
-      uint32_t phase = 0, it = 0, n = 0;
-      bool ok = true, issued = false;
+      constexpr uint32_t IDESC = make_idesc(2 * BM, BN);
+      int stage = 0, g = 0;  // operand stage, scale segment
+      uint32_t phase = 0, g_phase = 0, n = 0;
+      bool ok = true, issued = false, ready = false;
       for (int tile = first; ok && tile < p.tiles; tile += step, ++n) {
         const int a = n & 1;
         const bool got = wait_bar_cluster(bar_acc_empty(a), ((n >> 1) & 1u) ^ 1u, p.wait_limit,
@@ -254,20 +275,31 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           break;
         }
         tc_fence_after();
-        for (int kt = 0; kt < KT; ++kt, ++it) {
-          const int k = it & (P_SLOTS - 1);
-          const bool got_k = wait_bar_cluster(bar_sft_ready(k), (it / P_SLOTS) & 1u, p.wait_limit,
-                                              p.status, s_abort) &&
-                             wait_bar(bar_full(stage), phase, p.wait_limit, p.status, s_abort);
-          if (!__all_sync(0xffffffffu, got_k)) {
-            ok = false;
-            break;
+        for (int kt = 0; kt < KT; ++kt) {
+          const int i = kt % P_SEG;
+          if (!__all_sync(0xffffffffu, ready)) {
+            const bool got_k =
+                (i != 0 ||
+                 wait_bar(bar_sft_ready(g), g_phase, p.wait_limit, p.status, s_abort)) &&
+                wait_bar(bar_full(stage), phase, p.wait_limit, p.status, s_abort);
+            if (!__all_sync(0xffffffffu, got_k)) {
+              ok = false;
+              break;
+            }
           }
           tc_fence_after();
+          // look at the next slice's barriers before this slice's MMAs are
+          // issued: a wait takes about 90 cycles even when it is over
+          const bool last = i == P_SEG - 1 || kt == KT - 1;  // of the segment
+          const int stage1 = stage + 1 == STAGES ? 0 : stage + 1;
+          const int g1 = g + 1 == SEGS ? 0 : g + 1;
+          const bool ready_sf =
+              !last || mbar_test_wait(bar_sft_ready(g1), g1 ? g_phase : g_phase ^ 1u);
+          const bool ready_op = mbar_test_wait(bar_full(stage1), stage1 ? phase : phase ^ 1u);
           const uint64_t adesc = make_sdesc(sbase + stage * P_A_BYTES, 16, 1024, 2);
-          const uint64_t bdesc = make_sdesc(sbase + P_OFF_B + stage * P_B_BYTES, 16, 1024, 2);
-          const uint32_t t_sf = tmem + P_SF_COL + k * P_SLOT_COLS;
-          const uint32_t t_acc = tmem + a * P_BN;
+          const uint64_t bdesc = make_sdesc(sbase + L::OFF_B + stage * L::B_BYTES, 16, 1024, 2);
+          const uint32_t t_sf = tmem + L::SF_COL + g * L::SEG_COLS + i * L::SLICE_COLS;
+          const uint32_t t_acc = tmem + a * BN;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < BK / 32; ++kk)
@@ -275,11 +307,14 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                            IDESC | ((uint32_t)kk << 29) | ((uint32_t)kk << 4), t_sf, t_sf + 4,
                            (kt | kk) != 0 ? 1u : 0u);
             tc2_commit_both(bar_empty(stage));
+            if (last) tc2_commit_both(bar_sft_free(g));
             if (kt == KT - 1) tc2_commit_both(bar_acc_full(a));
           }
           __syncwarp();
           issued = true;
-          if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
+          ready = ready_sf && ready_op;
+          if (last && ++g == SEGS) { g = 0; g_phase ^= 1; }
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
       }
       if (ok) {
@@ -299,52 +334,72 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     // quarter holds every chunk).  A lane's 16 bytes of a chunk are its four
     // 32-row groups' words; a tile's B groups start at word g0 of its first
     // 128-row block and span up to three blocks.
-    const uint32_t t_q = tmem + ((uint32_t)((warp & 3) * 32) << 16) + P_SF_COL;
+    const uint32_t t_q = tmem + ((uint32_t)((warp & 3) * 32) << 16) + L::SF_COL;
     const uint32_t lead_ready = mapa_cluster(bar_sft_ready(0), 0);
-    int stage = 0, e_stage = 0;  // e: stage and parity of the slice P_SLOTS before
-    uint32_t phase = 0, e_phase = 0, it = 0;
+    int b = 0, g = 0;  // staged segment, tensor-memory segment
+    uint32_t b_phase = 0, g_phase = 0;
     bool ok = true;
+    uint32_t segs = 0;
     for (int tile = first; ok && tile < p.tiles; tile += step) {
       int64_t row0;
       int n0;
       tile_at(tile, row0, n0);
       const int g0 = (n0 >> 5) & 3;
-      for (int kt = 0; kt < KT; ++kt, ++it) {
-        const int k = it & (P_SLOTS - 1);
-        bool got = wait_bar(bar_sfs(stage), phase, p.wait_limit, p.status, s_abort);
-        if (it >= P_SLOTS) {
-          got = got && wait_bar(bar_empty(e_stage), e_phase, p.wait_limit, p.status, s_abort);
-          if (++e_stage == P_STAGES) { e_stage = 0; e_phase ^= 1; }
-        }
+      for (int kt = 0; kt < KT; kt += P_SEG, ++segs) {
+        bool got = wait_bar(bar_sfs_full(b), b_phase, p.wait_limit, p.status, s_abort);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
-        const uint8_t* sf = smem + P_OFF_SF + stage * P_SF_BYTES + lane * 16;
-        const uint32_t col = t_q + k * P_SLOT_COLS;
-        tmem_st_4(col, *reinterpret_cast<const uint4*>(sf));
-        uint32_t w[8];
+        // (a slice past K: whatever the buffer holds, never read by an MMA)
+        const uint8_t* sf = smem + L::OFF_SF + b * P_SF_BYTES + lane * 16;
+        uint4 wa[P_SEG];
+        uint32_t wb[P_SEG][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {  // group g0 + j: chunk (g0 + j) / 4, word (g0 + j) % 4
-          const int g = g0 + j;
-          w[j] = *reinterpret_cast<const uint32_t*>(sf + 512 * (1 + (g >> 2)) + 4 * (g & 3));
+        for (int i = 0; i < P_SEG; ++i) {
+          wa[i] = *reinterpret_cast<const uint4*>(sf + 512 * i);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {  // group g0 + j: block (g0 + j) / 4, word (g0 + j) % 4
+            const int gg = g0 + j;
+            wb[i][j] = *reinterpret_cast<const uint32_t*>(
+                sf + 512 * (P_SEG * (1 + (gg >> 2)) + i) + 4 * (gg & 3));
+          }
         }
-        tmem_st_4(col + 4, make_uint4(w[0], w[1], w[2], w[3]));
-        tmem_st_4(col + 8, make_uint4(w[4], w[5], w[6], w[7]));
+        got = wait_bar(bar_sft_free(g), g_phase ^ 1u, p.wait_limit, p.status, s_abort);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        const uint32_t col = t_q + g * L::SEG_COLS;
+#pragma unroll
+        for (int i = 0; i < P_SEG; ++i) {
+          tmem_st_4(col + i * L::SLICE_COLS, wa[i]);
+          tmem_st_4(col + i * L::SLICE_COLS + 4,
+                    make_uint4(wb[i][0], wb[i][1], wb[i][2], wb[i][3]));
+          if (BN > 128)
+            tmem_st_4(col + i * L::SLICE_COLS + 8,
+                      make_uint4(wb[i][4], wb[i][5], wb[i][6], wb[i][7]));
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (leader) mbar_arrive(bar_sft_ready(k));
-          else mbar_arrive_cluster(lead_ready + 8u * k);
+          if (leader) mbar_arrive(bar_sft_ready(g));
+          else mbar_arrive_cluster(lead_ready + 8u * g);
+          mbar_arrive(bar_sfs_free(b));
         }
-        if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
+        if (++b == P_SFS) { b = 0; b_phase ^= 1; }
+        if (++g == SEGS) { g = 0; g_phase ^= 1; }
       }
     }
+    // the commits that free the last segments have landed
+    if (ok)
+      for (uint32_t i = segs >= SEGS ? segs - SEGS : 0; i < segs; ++i)
+        wait_bar(bar_sft_free(i % SEGS), (i / SEGS) & 1u, p.wait_limit, p.status, s_abort);
     __syncwarp();
   } else if (warp == P_SF_WARP) {
     // ================= scale producer
-    int stage = 0;
+    int b = 0;
     uint32_t phase = 0, armed = 0, armed_parity = 0;
     bool ok = true;
     const int64_t last_a = (p.M - 1) >> 7;
@@ -355,32 +410,34 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       tile_at(tile, row0, n0);
       const uint8_t* at_a = p.sfx + min(row0 >> 7, last_a) * KT * 512;
       const int rb = n0 >> 7;
-      for (int kt = 0; kt < KT; ++kt) {
-        const bool got = wait_bar(bar_empty(stage), phase ^ 1, p.wait_limit, p.status, s_abort);
+      for (int kt = 0; kt < KT; kt += P_SEG) {
+        const bool got = wait_bar(bar_sfs_free(b), phase ^ 1, p.wait_limit, p.status, s_abort);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
         if (elect_one()) {
-          const uint32_t sf = sbase + P_OFF_SF + stage * P_SF_BYTES;
-          mbar_arrive_expect_tx(bar_sfs(stage), P_SF_BYTES);
-          bulk_copy_g2s(sf, at_a + (int64_t)kt * 512, 512, bar_sfs(stage));
+          const uint32_t sf = sbase + L::OFF_SF + b * P_SF_BYTES;
+          const uint32_t bytes = (uint32_t)min(P_SEG, KT - kt) * 512u;
+          mbar_arrive_expect_tx(bar_sfs_full(b), 4 * bytes);
+          bulk_copy_g2s(sf, at_a + (int64_t)kt * 512, bytes, bar_sfs_full(b));
 #pragma unroll
           for (int c = 0; c < 3; ++c)  // (blocks past the last one: copied again, not used)
-            bulk_copy_g2s(sf + 512 * (c + 1), p.sfw + ((int64_t)min(rb + c, last_b) * KT + kt) * 512,
-                          512, bar_sfs(stage));
+            bulk_copy_g2s(sf + 512 * P_SEG * (c + 1),
+                          p.sfw + ((int64_t)min(rb + c, last_b) * KT + kt) * 512, bytes,
+                          bar_sfs_full(b));
         }
         __syncwarp();
-        armed |= 1u << stage;
-        if (phase) armed_parity |= 1u << stage; else armed_parity &= ~(1u << stage);
-        if (++stage == P_STAGES) { stage = 0; phase ^= 1; }
+        armed |= 1u << b;
+        if (phase) armed_parity |= 1u << b; else armed_parity &= ~(1u << b);
+        if (++b == P_SFS) { b = 0; phase ^= 1; }
       }
     }
     if (!ok) {  // abort: this CTA's copies land before it leaves
       volatile int no_abort = 0;
-      for (int s = 0; s < P_STAGES; ++s)
+      for (int s = 0; s < P_SFS; ++s)
         if ((armed >> s) & 1u)
-          wait_bar(bar_sfs(s), (armed_parity >> s) & 1u, 1ll << 32, nullptr, &no_abort);
+          wait_bar(bar_sfs_full(s), (armed_parity >> s) & 1u, 1ll << 32, nullptr, &no_abort);
     }
     __syncwarp();
   } else {
@@ -388,7 +445,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const int q = warp & 3, half = (warp - 6) >> 2;
     const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16);
     const uint32_t lead_acc_empty = mapa_cluster(bar_acc_empty(0), 0);
-    const int nch = p.BN / 32;
+    constexpr int nch = BN / 32;
     uint32_t n = 0;
     for (int tile = first; tile < p.tiles; tile += step, ++n) {
       const int a = n & 1;
@@ -403,7 +460,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       for (int c = half; c < nch; c += 2) {
         const int col = n0 + 32 * c;
         uint32_t v[32], res[16];
-        tmem_ld_32(t_row + a * P_BN + 32 * c, v);
+        tmem_ld_32(t_row + a * BN + 32 * c, v);
         if (p.res && valid && col < p.N) {
           const uint16_t* src = p.res + row * p.N + col;
           const bool hi = col + 16 < p.N;
@@ -458,12 +515,16 @@ double pair_cycles(int64_t M, int N, int K, int* bn) {
   return best;
 }
 
-cudaError_t launch_pair(const uint8_t* xq, const uint8_t* wq, LinParams p, cudaStream_t stream) {
+template <int BN>
+static cudaError_t launch_pair_bn(const uint8_t* xq, const uint8_t* wq, LinParams p,
+                                  cudaStream_t stream) {
+  using L = Pair<BN>;
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   static int max_clusters[64];
   static uint64_t configured[64] = {0};  // context id the attribute was set in
+  auto kern = linear_pair_kernel<BN>;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -473,18 +534,18 @@ cudaError_t launch_pair(const uint8_t* xq, const uint8_t* wq, LinParams p, cudaS
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(P_THREADS);
-  cfg.dynamicSmemBytes = P_ALLOC;
+  cfg.dynamicSmemBytes = L::ALLOC;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const uint64_t ctx = context_id();
   if (ctx == 0 || configured[dev] != ctx) {
-    const cudaError_t err = cudaFuncSetAttribute(
-        linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P_ALLOC);
+    const cudaError_t err =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
     if (err != cudaSuccess) return err;
     cfg.gridDim = dim3(2 * 64);
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
@@ -492,20 +553,29 @@ cudaError_t launch_pair(const uint8_t* xq, const uint8_t* wq, LinParams p, cudaS
     configured[dev] = context_id();
   }
   if (max_clusters[dev] <= 0) return cudaErrorNotSupported;
-  p.tiles_n = (int)ceil_div(p.N, p.BN);
+  p.tiles_n = (int)ceil_div(p.N, BN);
   const int64_t tiles = ceil_div(p.M, 2 * BM) * p.tiles_n;
   if (tiles >= (1ll << 31)) return cudaErrorNotSupported;
   p.tiles = (int)tiles;
   p.v32 = (((uintptr_t)p.out | (uintptr_t)p.res) & 31u) == 0;
   CUtensorMap tmX, tmW;
   if (!make_map(&tmX, xq, (uint64_t)p.K, (uint64_t)p.M, BK, BM) ||
-      !make_map(&tmW, wq, (uint64_t)p.K, (uint64_t)p.N, BK, (uint32_t)(p.BN / 2)))
+      !make_map(&tmW, wq, (uint64_t)p.K, (uint64_t)p.N, BK, BN / 2))
     return cudaErrorInvalidValue;
   const int clusters = (int)std::min<int64_t>(
       {tiles, (int64_t)max_clusters[dev], (int64_t)std::max(1, num_sms() / 2)});
   cfg.gridDim = dim3(2 * clusters);
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_pair_kernel, tmX, tmW, p);
+  return cudaLaunchKernelEx(&cfg, kern, tmX, tmW, p);
+}
+
+cudaError_t launch_pair(const uint8_t* xq, const uint8_t* wq, const LinParams& p, int bn,
+                        cudaStream_t stream) {
+  switch (bn) {
+    case 224: return launch_pair_bn<224>(xq, wq, p, stream);
+    case 192: return launch_pair_bn<192>(xq, wq, p, stream);
+    default: return launch_pair_bn<128>(xq, wq, p, stream);
+  }
 }
 
 }  // namespace linear
