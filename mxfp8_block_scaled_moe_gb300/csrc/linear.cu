@@ -49,15 +49,6 @@ __host__ __device__ inline Smem smem_layout(int NT, int stages) {
   return s;
 }
 
-__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
 __device__ __forceinline__ void tmem_st_1(uint32_t taddr, uint32_t v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
 }
@@ -81,8 +72,11 @@ __device__ __forceinline__ void finish_token(const LinParams& p, int64_t t, int 
                                              float4 v, const float4& bias, uint2 res) {
   const int n = n0 + 4 * lane;
   const bool in = n < p.N;
-  float a[4] = {v.x + bias.x, v.y + bias.y, v.z + bias.z, v.w + bias.w};
-  activate_all(p.act, a);
+  F2 a2[2] = {add2(f2(v.x, v.y), f2(bias.x, bias.y)), add2(f2(v.z, v.w), f2(bias.z, bias.w))};
+  activate_all(p.act, a2);
+  float a[4];
+  unpack(a2[0], a[0], a[1]);
+  unpack(a2[1], a[2], a[3]);
   if (p.out) {
     if (!in) return;
     a[0] += bf16_bits_to_float(res.x & 0xFFFFu);

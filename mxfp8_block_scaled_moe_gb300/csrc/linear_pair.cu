@@ -16,9 +16,9 @@
 // epilogue of a tile (bias, activation, residual, stores) runs under the next
 // tile's MMAs, which matters when K is short: a tile of K = 1152 is 36 MMAs.
 //
-// Roles (480 threads per CTA): warp 0 producer, warp 1 MMA issuer (even CTA),
-// warps 2-5 scale-factor writers, warps 6-13 epilogue (two per TMEM lane
-// quarter, 32-column chunks in turn), warp 14 scale producer (bulk copies of
+// Roles (736 threads per CTA): warp 0 producer, warp 1 MMA issuer (even CTA),
+// warps 2-5 scale-factor writers, warps 6-21 epilogue (four per TMEM lane
+// quarter, pieces of 16 or 32 columns in turn), warp 22 scale producer (bulk copies of
 // the scale chunks; on warp 0 their issue slowed the operand loads).  The
 // scales move in segments of two k-slices: a writer's waits, reads, stores and
 // arrival take about 550 cycles however much they move, more than a slice's MMAs.
@@ -38,7 +38,7 @@
 namespace mxmoe {
 namespace linear {
 
-constexpr int P_EPI_WARPS = 8;
+constexpr int P_EPI_WARPS = 16;  // a multiple of 4
 constexpr int P_SF_WARP = 6 + P_EPI_WARPS;  // scale producer
 constexpr int P_THREADS = 32 * (P_SF_WARP + 1);
 constexpr int P_A_BYTES = BM * BK;
@@ -59,7 +59,8 @@ struct Pair {
   static constexpr int SEGS = (TMEM_COLS - SF_COL) / SEG_COLS >= 4 ? 4 : 2;
   static constexpr int OFF_B = STAGES * P_A_BYTES;
   static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
-  static constexpr int OFF_BAR = OFF_SF + P_SFS * P_SF_BYTES;
+  static constexpr int OFF_BIAS = OFF_SF + P_SFS * P_SF_BYTES;  // 64 fp32 per epilogue warp
+  static constexpr int OFF_BAR = OFF_BIAS + P_EPI_WARPS * 256;
   // full, empty [STAGES], sfs_full, sfs_free [P_SFS], sft_ready, sft_free [SEGS],
   // acc_full, acc_empty [2], drain
   static constexpr int NUM_BARS = 2 * STAGES + 2 * P_SFS + 2 * SEGS + 5;
@@ -69,72 +70,80 @@ struct Pair {
   static_assert(B_BYTES % 1024 == 0 && ALLOC <= 232448, "shared memory");
 };
 
-// 32 columns of one row: bias, activation, residual, rounding, store.
-// n: first column (a multiple of 32, < N); the second half may lie past N.
-__device__ __forceinline__ void finish_chunk(const LinParams& p, int64_t row, bool valid, int n,
-                                             const uint32_t (&v)[32], const uint32_t (&res)[16]) {
-  const bool hi = n + 16 < p.N;  // uniform
-  float a[32];
+// 16 columns of one row to bf16: bias, activation, residual, rounding, store.
+// n: first column (a multiple of 16, < N).  bias: 16 fp32 in shared memory or null.
+__device__ __forceinline__ void finish_bf16(const LinParams& p, int64_t row, bool valid, int n,
+                                            const uint32_t (&v)[16], const uint32_t (&res)[8],
+                                            const float4* bias) {
+  F2 a[8];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) a[i] = __uint_as_float(v[i]);
-  if (p.bias) {
-    if (p.bias32) {
-      const float4* b = reinterpret_cast<const float4*>(static_cast<const float*>(p.bias) + n);
+  for (int i = 0; i < 8; ++i) a[i] = f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+  if (bias) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < 4 || hi) {
-          const float4 w = __ldg(b + i);
-          a[4 * i] += w.x; a[4 * i + 1] += w.y; a[4 * i + 2] += w.z; a[4 * i + 3] += w.w;
-        }
-    } else {
-      const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + n);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < 2 || hi) {
-          const uint4 w = __ldg(b + i);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            a[8 * i + 2 * j] += bf16_bits_to_float(u[j] & 0xFFFFu);
-            a[8 * i + 2 * j + 1] += bf16_bits_to_float(u[j] >> 16);
-          }
-        }
+    for (int i = 0; i < 4; ++i) {
+      const float4 w = bias[i];
+      a[2 * i] = add2(a[2 * i], f2(w.x, w.y));
+      a[2 * i + 1] = add2(a[2 * i + 1], f2(w.z, w.w));
     }
   }
   activate_all(p.act, a);
-  if (p.out) {
-    uint32_t o[16];
-    if (p.res) {
+  if (p.res) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        a[2 * i] += bf16_bits_to_float(res[i] & 0xFFFFu);
-        a[2 * i + 1] += bf16_bits_to_float(res[i] >> 16);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = cvt_bf16x2(a[2 * i], a[2 * i + 1]);
-    if (!valid) return;
-    uint16_t* dst = p.out + row * p.N + n;
-    if (p.v32) {
-      st_v8(dst, *reinterpret_cast<const uint32_t(*)[8]>(&o[0]));
-      if (hi) st_v8(dst + 16, *reinterpret_cast<const uint32_t(*)[8]>(&o[8]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < 2 || hi) st_v4(dst + 8 * i, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
-    }
-    return;
+    for (int i = 0; i < 8; ++i) a[i] = add2(a[i], bf16x2_f2(res[i]));
   }
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (i < 16 || hi) m = umax(m, __float_as_uint(a[i]) & 0x7FFFFFFFu);
-  const uint32_t sb = e8m0_from_amax_bits(m);
-  const float inv = inv_scale_from_e8m0(sb);
   uint32_t o[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    o[i] = cvt_e4m3x4(a[4 * i] * inv, a[4 * i + 1] * inv, a[4 * i + 2] * inv, a[4 * i + 3] * inv);
+  for (int i = 0; i < 8; ++i) {
+    float x, y;
+    unpack(a[i], x, y);
+    o[i] = cvt_bf16x2(x, y);
+  }
+  if (!valid) return;
+  uint16_t* dst = p.out + row * p.N + n;
+  if (p.v32) {
+    st_v8(dst, o);
+  } else {
+    st_v4(dst, make_uint4(o[0], o[1], o[2], o[3]));
+    st_v4(dst + 8, make_uint4(o[4], o[5], o[6], o[7]));
+  }
+}
+
+// 32 columns of one row (one MX block) to MXFP8: bias, activation, scale, payload.
+// n: first column (a multiple of 32, < N); the second half may lie past N.
+__device__ __forceinline__ void finish_mx(const LinParams& p, int64_t row, bool valid, int n,
+                                          const uint32_t (&v)[32], const float4* bias) {
+  const bool hi = n + 16 < p.N;  // uniform
+  F2 a[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] = f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+  if (bias) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 w = bias[i];
+      a[2 * i] = add2(a[2 * i], f2(w.x, w.y));
+      a[2 * i + 1] = add2(a[2 * i + 1], f2(w.z, w.w));
+    }
+  }
+  activate_all(p.act, a);
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < 8 || hi) {
+      float x, y;
+      unpack(a[i], x, y);
+      m = absmax3(m, x, y);
+    }
+  const uint32_t sb = e8m0_from_amax_bits(__float_as_uint(m));
+  const float inv = inv_scale_from_e8m0(sb);
+  const F2 inv2 = f2(inv, inv);
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float x, y, z, w;
+    unpack(mul2(a[2 * i], inv2), x, y);
+    unpack(mul2(a[2 * i + 1], inv2), z, w);
+    o[i] = cvt_e4m3x4(x, y, z, w);
+  }
   if (!valid) return;
   uint8_t* dst = p.oq + row * p.N + n;
   st_v4(dst, make_uint4(o[0], o[1], o[2], o[3]));
@@ -145,7 +154,8 @@ __device__ __forceinline__ void finish_chunk(const LinParams& p, int64_t row, bo
     for (int jj = j + 1; jj < 4 * KT; ++jj) p.os[tiled_scale_offset(row, jj, KT)] = 127;
 }
 
-template <int BN>
+// kMX: MXFP8 result (32-column pieces), else bf16 (16-column pieces)
+template <int BN, bool kMX>
 __global__ void __launch_bounds__(P_THREADS, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmW, const LinParams p) {
@@ -351,18 +361,26 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           ok = false;
           break;
         }
-        // (a slice past K: whatever the buffer holds, never read by an MMA)
+        // (a slice past K: whatever the buffer holds, never read by an MMA).
+        // The lane's words of all three B blocks, then those from g0 on: 16-byte
+        // reads, where word reads at this stride meet four-way bank conflicts.
         const uint8_t* sf = smem + L::OFF_SF + b * P_SF_BYTES + lane * 16;
         uint4 wa[P_SEG];
         uint32_t wb[P_SEG][8];
 #pragma unroll
         for (int i = 0; i < P_SEG; ++i) {
           wa[i] = *reinterpret_cast<const uint4*>(sf + 512 * i);
+          uint32_t w[12];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {  // group g0 + j: block (g0 + j) / 4, word (g0 + j) % 4
-            const int gg = g0 + j;
-            wb[i][j] = *reinterpret_cast<const uint32_t*>(
-                sf + 512 * (P_SEG * (1 + (gg >> 2)) + i) + 4 * (gg & 3));
+          for (int c = 0; c < 3; ++c) {
+            const uint4 u = *reinterpret_cast<const uint4*>(sf + 512 * (P_SEG * (1 + c) + i));
+            w[4 * c] = u.x; w[4 * c + 1] = u.y; w[4 * c + 2] = u.z; w[4 * c + 3] = u.w;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t even = (g0 & 2) ? w[j + 2] : w[j];
+            const uint32_t odd = (g0 & 2) ? w[j + 3] : w[j + 1];
+            wb[i][j] = (g0 & 1) ? odd : even;
           }
         }
         got = wait_bar(bar_sft_free(g), g_phase ^ 1u, p.wait_limit, p.status, s_abort);
@@ -441,11 +459,16 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     }
     __syncwarp();
   } else {
-    // ================= epilogue
-    const int q = warp & 3, half = (warp - 6) >> 2;
+    // ================= epilogue: a warp per TMEM lane quarter and group, the
+    // tile's column pieces in turn
+    constexpr int PC = kMX ? 32 : 16, PIECES = BN / PC, GRPS = P_EPI_WARPS / 4;
+    static_assert(PIECES >= GRPS, "every epilogue warp reads the accumulator");
+    const int q = warp & 3, grp = (warp - 6) >> 2;
     const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16);
     const uint32_t lead_acc_empty = mapa_cluster(bar_acc_empty(0), 0);
-    constexpr int nch = BN / 32;
+    // the bias of this warp's pieces of a tile, in piece order
+    static_assert((PIECES + GRPS - 1) / GRPS * PC <= 64, "bias staging");
+    float* s_bias = reinterpret_cast<float*>(smem + L::OFF_BIAS) + (warp - 6) * 64;
     uint32_t n = 0;
     for (int tile = first; tile < p.tiles; tile += step, ++n) {
       const int a = n & 1;
@@ -454,25 +477,42 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       tile_at(tile, row0, n0);
       const int64_t row = row0 + q * 32 + lane;
       const bool valid = row < p.M;
+      if (p.bias) {
+        __syncwarp();  // the tile before has been read
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int slot = lane + 32 * i;  // piece grp + GRPS (slot / PC), column slot % PC
+          const int col = n0 + PC * (grp + GRPS * (slot / PC)) + slot % PC;
+          if (col < n0 + BN && col < p.N)
+            s_bias[slot] = p.bias32 ? __ldg(static_cast<const float*>(p.bias) + col)
+                                    : bf16_bits_to_float(
+                                          __ldg(static_cast<const uint16_t*>(p.bias) + col));
+        }
+        __syncwarp();
+      }
       const bool got = wait_bar(bar_acc_full(a), (n >> 1) & 1u, p.wait_limit, p.status, s_abort);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
-      for (int c = half; c < nch; c += 2) {
-        const int col = n0 + 32 * c;
-        uint32_t v[32], res[16];
-        tmem_ld_32(t_row + a * BN + 32 * c, v);
-        if (p.res && valid && col < p.N) {
+      const float4* bias = p.bias ? reinterpret_cast<const float4*>(s_bias) : nullptr;
+      for (int c = grp; c < PIECES; c += GRPS) {
+        const int col = n0 + PC * c;
+        uint32_t v[PC];
+        if constexpr (kMX) tmem_ld_32(t_row + a * BN + PC * c, v);
+        else tmem_ld_16(t_row + a * BN + PC * c, v);
+        uint32_t res[8];
+        if (!kMX && p.res && valid && col < p.N) {
           const uint16_t* src = p.res + row * p.N + col;
-          const bool hi = col + 16 < p.N;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < 2 || hi) {
-              const uint4 u = *reinterpret_cast<const uint4*>(src + 8 * i);
-              res[4 * i] = u.x; res[4 * i + 1] = u.y; res[4 * i + 2] = u.z; res[4 * i + 3] = u.w;
-            }
+          if (p.v32) {
+            ld_v8(src, res);
+          } else {
+            const uint4 u = *reinterpret_cast<const uint4*>(src);
+            const uint4 w = *reinterpret_cast<const uint4*>(src + 8);
+            res[0] = u.x; res[1] = u.y; res[2] = u.z; res[3] = u.w;
+            res[4] = w.x; res[5] = w.y; res[6] = w.z; res[7] = w.w;
+          }
         }
         tmem_ld_wait();
-        if (c + 2 >= nch) {  // this warp's last read of the accumulator
+        if (c + GRPS >= PIECES) {  // this warp's last read of the accumulator
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -480,7 +520,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             else mbar_arrive_cluster(lead_acc_empty + 8u * a);
           }
         }
-        if (col < p.N) finish_chunk(p, row, valid, col, v, res);  // warp-uniform
+        if (col < p.N) {  // warp-uniform
+          if constexpr (kMX) finish_mx(p, row, valid, col, v, bias);
+          else finish_bf16(p, row, valid, col, v, res, bias);
+        }
+        if (bias) bias += PC / 4;
       }
     }
   }
@@ -515,7 +559,7 @@ double pair_cycles(int64_t M, int N, int K, int* bn) {
   return best;
 }
 
-template <int BN>
+template <int BN, bool kMX>
 static cudaError_t launch_pair_bn(const uint8_t* xq, const uint8_t* wq, LinParams p,
                                   cudaStream_t stream) {
   using L = Pair<BN>;
@@ -524,7 +568,7 @@ static cudaError_t launch_pair_bn(const uint8_t* xq, const uint8_t* wq, LinParam
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   static int max_clusters[64];
   static uint64_t configured[64] = {0};  // context id the attribute was set in
-  auto kern = linear_pair_kernel<BN>;
+  auto kern = linear_pair_kernel<BN, kMX>;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -571,10 +615,17 @@ static cudaError_t launch_pair_bn(const uint8_t* xq, const uint8_t* wq, LinParam
 
 cudaError_t launch_pair(const uint8_t* xq, const uint8_t* wq, const LinParams& p, int bn,
                         cudaStream_t stream) {
+  const bool mx = p.out == nullptr;
   switch (bn) {
-    case 224: return launch_pair_bn<224>(xq, wq, p, stream);
-    case 192: return launch_pair_bn<192>(xq, wq, p, stream);
-    default: return launch_pair_bn<128>(xq, wq, p, stream);
+    case 224:
+      return mx ? launch_pair_bn<224, true>(xq, wq, p, stream)
+                : launch_pair_bn<224, false>(xq, wq, p, stream);
+    case 192:
+      return mx ? launch_pair_bn<192, true>(xq, wq, p, stream)
+                : launch_pair_bn<192, false>(xq, wq, p, stream);
+    default:
+      return mx ? launch_pair_bn<128, true>(xq, wq, p, stream)
+                : launch_pair_bn<128, false>(xq, wq, p, stream);
   }
 }
 
