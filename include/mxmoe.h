@@ -458,7 +458,8 @@ mxmoe_status mxfp8_linear_fused(const uint16_t* x, const uint8_t* xq, const uint
  *   counts_in  NULL or int64 [E], non-negative
  *   loss       fp32 [1];  counts int64 [E]
  *   dlogits    fp32 [T, E] contiguous; NULL: no gradient
- *   ws         moe_balance_loss_workspace_size(T, E) bytes, 16-byte aligned
+ *   ws         moe_balance_loss_workspace_size(T, E) bytes, 16-byte aligned (0 for
+ *              few tokens: then it may be NULL)
  * With n = 0 or no assignment, loss and gradient are 0.  A logit of -inf has
  * probability 0, also in a row of nothing else; a masked token's logits are not
  * read.  Sums run in a fixed order: the same inputs give the same bits.

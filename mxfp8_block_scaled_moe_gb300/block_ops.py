@@ -219,6 +219,10 @@ def moe_balance_loss_workspace_size(T: int, E: int) -> int:
     return int(_lib.load().moe_balance_loss_workspace_size(T, E))
 
 
+# up to this many tokens the loss is one kernel without a workspace
+_BALANCE_ONE_KERNEL = 1024
+
+
 def _balance(logits, topk_ids, mask, counts, coef, grad):
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor (the library has no CPU path)")
@@ -246,7 +250,8 @@ def _balance(logits, topk_ids, mask, counts, coef, grad):
         counts_ptr = counts.data_ptr()
     dev = logits.device
     lib = _lib.load()
-    ws = torch.empty(lib.moe_balance_loss_workspace_size(T, E), dtype=torch.uint8, device=dev)
+    need = 0 if T <= _BALANCE_ONE_KERNEL else lib.moe_balance_loss_workspace_size(T, E)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     loss = torch.empty((), dtype=torch.float32, device=dev)
     own_counts = torch.empty(E, dtype=torch.int64, device=dev)
     out = {"loss": loss, "counts": own_counts}
@@ -255,8 +260,8 @@ def _balance(logits, topk_ids, mask, counts, coef, grad):
         grad_ptr = d.data_ptr()
     rc = lib.moe_balance_loss(
         logits.data_ptr(), ldl, topk_ids.data_ptr(), mask_ptr, counts_ptr, T, E,
-        topk_ids.shape[1], coef, loss.data_ptr(), own_counts.data_ptr(), grad_ptr, ws.data_ptr(),
-        ws.numel(), _stream(logits))
+        topk_ids.shape[1], coef, loss.data_ptr(), own_counts.data_ptr(), grad_ptr,
+        ws.data_ptr() if need else None, need, _stream(logits))
     if rc:
         _lib.check("moe_balance_loss", rc)
     return out

@@ -767,7 +767,8 @@ mxmoe_status moe_balance_loss(const float* logits, int64_t ldl, const int32_t* t
   if (!aligned(loss, 4) || !aligned(counts, 8) || !aligned(logits, 4) || !aligned(topk_ids, 4) ||
       !aligned(counts_in, 8) || !aligned(dlogits, 4) || !aligned16(ws))
     return MXMOE_ERR_ALIGN;
-  if (!ws || ws_bytes < balance_workspace_bytes(T, E)) return MXMOE_ERR_WORKSPACE;
+  const size_t need = balance_workspace_bytes(T, E);
+  if (need && (!ws || ws_bytes < need)) return MXMOE_ERR_WORKSPACE;
   return from_cuda(launch_balance_loss(logits, ldl, topk_ids, mask, counts_in, T, E, k, coef, loss,
                                        counts, dlogits, (uint32_t*)ws, (cudaStream_t)stream));
 }

@@ -133,8 +133,8 @@ def _bal(lib, **kw):
     (dict(T=-1), 3), (dict(E=0), 3), (dict(k=0), 3), (dict(k=9), 3), (dict(ldl=7), 3),
     (dict(T=1 << 30), 3), (dict(E=1025, ldl=1025), 4), (dict(E=64, ldl=64, k=33), 4),
     (dict(logits=NUL), 1), (dict(ids=NUL), 1), (dict(loss=NUL), 1), (dict(counts=NUL), 1),
-    (dict(logits=ODD), 2), (dict(counts=ODD), 2), (dict(ws=ODD), 2), (dict(ws=NUL), 5),
-    (dict(ws_bytes=8), 5)])
+    (dict(logits=ODD), 2), (dict(counts=ODD), 2), (dict(ws=ODD), 2), (dict(T=4096, ws=NUL), 5),
+    (dict(T=4096, ws_bytes=8), 5)])
 def test_balance_refusals(lib, kw, code):
     assert _bal(lib, **kw) == code
 
@@ -145,6 +145,9 @@ def test_workspace_sizes(lib):
     assert lib.mxfp8_linear_fused_workspace_size(-1, 64) == 0
     assert lib.moe_balance_loss_workspace_size(16384, 128) >= 128 * 4
     assert lib.moe_balance_loss_workspace_size(4, 2000) == 0
+    # one kernel without a workspace up to 1024 tokens
+    assert lib.moe_balance_loss_workspace_size(1024, 128) == 0
+    assert lib.moe_balance_loss_workspace_size(1025, 128) > 0
 
 
 def test_bindings_refuse():
