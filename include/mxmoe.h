@@ -415,8 +415,8 @@ mxmoe_status mx_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* re
  *   out     = bf16(v + residual), rounded once;  or
  *   out_q, out_s = MX-quant(v) along N (v in fp32), what the next product reads
  *
- *   x          bf16 [M, K], MX-quantized into the workspace (the rule of
- *              mx_quantize_3d); or NULL, and then
+ *   x          bf16 [M, K], MX-quantized first (the rule of mx_quantize_3d);
+ *              or NULL, and then
  *   xq, xs     e4m3 [M, K] and its scales in the MMA layout (mx_add_rmsnorm_quant
  *              with mma_layout, or out_q / out_s of another call)
  *   wq, ws     e4m3 [N, K] and its scales in the MMA layout
@@ -428,12 +428,14 @@ mxmoe_status mx_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* re
  *   out_q      e4m3 [M, N]
  *   out_s      its scales in the MMA layout, ceil(M/128) * ceil(N/128) * 512
  *              bytes, rows past M unwritten
- *   workspace  mxfp8_linear_fused_workspace_size(M, K) bytes, 256-byte aligned,
- *              when x is given; unused otherwise
+ *   workspace  mxfp8_linear_fused_workspace_size(M, N, K) bytes for the current
+ *              device, 256-byte aligned, when x is given (0 where few rows are
+ *              quantized in the product's kernel: then it may be NULL); unused
+ *              otherwise
  * All pointers 16-byte aligned.  Requires K % 16 == 0, N % 16 == 0, M < 2^24.
  * M == 0 is a no-op.
  */
-size_t mxfp8_linear_fused_workspace_size(int64_t M, int64_t K);
+size_t mxfp8_linear_fused_workspace_size(int64_t M, int64_t N, int64_t K);
 mxmoe_status mxfp8_linear_fused(const uint16_t* x, const uint8_t* xq, const uint8_t* xs,
                                 const uint8_t* wq, const uint8_t* ws, int64_t M, int64_t N,
                                 int64_t K, const void* bias, int bias_fp32, int act,

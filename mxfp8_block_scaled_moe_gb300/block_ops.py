@@ -100,8 +100,8 @@ def mx_add_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, bf16_out: 
     return out
 
 
-def mxfp8_linear_fused_workspace_size(M: int, K: int) -> int:
-    return int(_lib.load().mxfp8_linear_fused_workspace_size(M, K))
+def mxfp8_linear_fused_workspace_size(M: int, N: int, K: int) -> int:
+    return int(_lib.load().mxfp8_linear_fused_workspace_size(M, N, K))
 
 
 def mxfp8_linear_fused(x, wq, ws_mma, bias=None, act=None, residual=None, mx_out: bool = False,
@@ -139,10 +139,11 @@ def mxfp8_linear_fused(x, wq, ws_mma, bias=None, act=None, residual=None, mx_out
         xq_ptr, xs_ptr = xq.data_ptr(), xs.data_ptr()
     else:
         x_ptr = x.data_ptr()
-        need = mxfp8_linear_fused_workspace_size(M, K)
-        if workspace is None:
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        need = mxfp8_linear_fused_workspace_size(M, N, K)
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        if need:
+            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if act not in ACTIVATIONS:
         raise ValueError(f"act: expected one of {sorted(k for k in ACTIVATIONS if k)}, got {act!r}")
     bias_ptr, bias32 = None, 0
@@ -202,9 +203,9 @@ class MXFP8FusedLinear:
         return cls(*mx_quantize_3d(w), bias=bias, act=act)
 
     def workspace(self, M: int, device):
-        need = mxfp8_linear_fused_workspace_size(M, self.K)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        need = mxfp8_linear_fused_workspace_size(M, self.N, self.K)
+        if need and (self._ws is None or self._ws.numel() < need):
+            self._ws = torch.empty(need, dtype=torch.uint8, device=device)
         return self._ws
 
     def __call__(self, x, residual=None, mx_out: bool = False, out=None):

@@ -703,8 +703,10 @@ mxmoe_status mx_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* re
 // Workspace of mxfp8_linear_fused with bf16 input: xq [M, K] | xs in the MMA layout.
 static size_t fused_xs_offset(int64_t M, int64_t K) { return align256((size_t)M * K); }
 
-size_t mxfp8_linear_fused_workspace_size(int64_t M, int64_t K) {
-  if (!linear_shape_ok(M, 16, K) || M >= (1ll << 24)) return 0;
+size_t mxfp8_linear_fused_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (!linear_shape_ok(M, N, K) || M >= (1ll << 24) || M == 0 ||
+      linear_quantizes_in_place(M, (int)N, (int)K))
+    return 0;
   return fused_xs_offset(M, K) +
          align256((size_t)((M + 127) / 128) * (size_t)((K + 127) / 128) * 512);
 }
@@ -734,20 +736,23 @@ mxmoe_status mxfp8_linear_fused(const uint16_t* x, const uint8_t* xq, const uint
   if (x) {
     if (xq || xs) return MXMOE_ERR_UNSUPPORTED;  // one input form
     MXMOE_CHECK_PTR(x);
-    if (!workspace || ws_bytes < mxfp8_linear_fused_workspace_size(M, K))
-      return MXMOE_ERR_WORKSPACE;
-    if (!aligned(workspace, 256)) return MXMOE_ERR_ALIGN;
-    uint8_t* base = (uint8_t*)workspace;
-    if (launch_mx_quantize_tiled(x, M, K, base, base + fused_xs_offset(M, K), nullptr, st) !=
-        cudaSuccess)
-      return MXMOE_ERR_CUDA;
-    xq = base;
-    xs = base + fused_xs_offset(M, K);
+    if (!linear_quantizes_in_place(M, (int)N, (int)K)) {
+      if (!workspace || ws_bytes < mxfp8_linear_fused_workspace_size(M, N, K))
+        return MXMOE_ERR_WORKSPACE;
+      if (!aligned(workspace, 256)) return MXMOE_ERR_ALIGN;
+      uint8_t* base = (uint8_t*)workspace;
+      if (launch_mx_quantize_tiled(x, M, K, base, base + fused_xs_offset(M, K), nullptr, st) !=
+          cudaSuccess)
+        return MXMOE_ERR_CUDA;
+      xq = base;
+      xs = base + fused_xs_offset(M, K);
+      x = nullptr;
+    }
   } else {
     MXMOE_CHECK_PTR(xq);
     MXMOE_CHECK_PTR(xs);
   }
-  return from_cuda(launch_linear_fused(xq, xs, wq, ws, M, (int)N, (int)K, bias, bias_fp32 != 0,
+  return from_cuda(launch_linear_fused(x, xq, xs, wq, ws, M, (int)N, (int)K, bias, bias_fp32 != 0,
                                        act, residual, out, out_q, out_s, st));
 }
 

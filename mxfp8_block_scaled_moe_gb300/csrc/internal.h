@@ -135,13 +135,15 @@ cudaError_t launch_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void*
                                      int H, uint16_t* y, uint8_t* q, uint8_t* s, bool tiled,
                                      cudaStream_t stream);
 
-// MXFP8 product with bias, activation and residual (linear.cu).  Scales in the
-// MMA layout; bias, residual nullable; either out (bf16) or oq / os (MXFP8).
+// MXFP8 product with bias, activation and residual (linear.cu).  Either x (bf16,
+// only where linear_quantizes_in_place) or xq / xs; scales in the MMA layout;
+// bias, residual nullable; either out (bf16) or oq / os (MXFP8).
+bool linear_quantizes_in_place(int64_t M, int N, int K);
 enum : int { ACT_NONE = 0, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU, ACT_COUNT };
-cudaError_t launch_linear_fused(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq,
-                                const uint8_t* ws, int64_t M, int N, int K, const void* bias,
-                                bool bias32, int act, const uint16_t* residual, uint16_t* out,
-                                uint8_t* oq, uint8_t* os, cudaStream_t stream);
+cudaError_t launch_linear_fused(const uint16_t* x, const uint8_t* xq, const uint8_t* xs,
+                                const uint8_t* wq, const uint8_t* ws, int64_t M, int N, int K,
+                                const void* bias, bool bias32, int act, const uint16_t* residual,
+                                uint16_t* out, uint8_t* oq, uint8_t* os, cudaStream_t stream);
 
 // Load-balance loss, counts and the logits' gradient (balance.cu).  mask,
 // counts_in, dlogits nullable.

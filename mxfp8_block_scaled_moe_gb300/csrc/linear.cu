@@ -14,10 +14,18 @@
 // partials of a token in split order through distributed shared memory.  One
 // launch, no partial sums in device memory, the same bits in every run.
 //
-// Roles (320 threads): warp 0 producer (TMA of both operand tiles, bulk
-// copies of their scale chunks), warp 1 MMA issuer, warps 2-5 scale-factor
-// writers (shared memory -> TMEM), warps 2-9 accumulator -> shared memory,
-// all warps the epilogue (a warp per token, 4 columns of n per lane).
+// Roles (320 threads): warp 0 producer (TMA of both operand tiles, bulk copies
+// of their scale chunks, SEG k-slices per copy), warp 1 MMA issuer, warps 2-5
+// scale-factor writers (shared memory -> TMEM), warps 2-9 accumulator -> shared
+// memory, all warps the epilogue (a warp per token, 4 columns of n per lane).
+//
+// Few tokens.  The bytes are the weights', the time is latency: a CTA has some ten
+// k-slices.  So every CTA asks for its first weights before it waits for the
+// kernel before it; scales move eight slices at a time (slice by slice, the
+// writers' chain took 790 cycles per slice); the residual is loaded before the
+// mainloop; and a few bf16 tokens are quantized in place (kQuant): warps 2-9
+// turn the CTA's K range of x into e4m3 tiles and scales, where TMA would have
+// put them, while the first weights arrive, which saves a launch.
 //
 // Every mbarrier wait is bounded as in gemm.cu.
 #include "linear.cuh"
@@ -29,22 +37,28 @@ constexpr int WM = 128;              // weight rows per CTA
 constexpr int W_BYTES = WM * BK;     // 16 KB per k-slice
 constexpr int WARPS = 10;
 constexpr int L_THREADS = 32 * WARPS;
-constexpr int DRAIN_WARPS = 8;       // accumulator -> shared memory
-constexpr int MAX_STAGES = 6;
+constexpr int DRAIN_WARPS = 8;       // accumulator -> shared memory, quantizing
+constexpr int MAX_STAGES = 5;
 constexpr int MAX_SPLIT = 8;
+constexpr int SEG = 8;               // k-slices per scale segment (two segments staged)
+constexpr int Q_SLICES = 12;         // kQuant: most k-slices per CTA (x resident)
+constexpr int Q_ROWS = 32;           // kQuant: most rows
+constexpr int NUM_BARS = 2 * MAX_STAGES + 8 + 1;
 
-// Shared-memory layout (runtime NT and stage count).
+// Shared memory: weight stages, token tiles (per stage, or all of the CTA's
+// slices), two scale segments of the weights (and of the tokens, or all of the
+// CTA's slices), barriers.
 struct Smem {
   int x, sfw, sfx, bar, misc, total;
 };
-__host__ __device__ inline Smem smem_layout(int NT, int stages) {
+__host__ __device__ inline Smem smem_layout(int NT, int stages, bool quant) {
   Smem s;
   const int nx = NT > 128 ? 2 : 1;  // 128-row scale blocks of the token tile
   s.x = stages * W_BYTES;
-  s.sfw = s.x + stages * NT * BK;
-  s.sfx = s.sfw + stages * 512;
-  s.bar = s.sfx + stages * nx * 512;
-  s.misc = s.bar + (3 * MAX_STAGES + 1) * 8;
+  s.sfw = s.x + (quant ? Q_SLICES : stages) * NT * BK;
+  s.sfx = s.sfw + 2 * SEG * 512;
+  s.bar = s.sfx + (quant ? Q_SLICES : 2 * SEG * nx) * 512;
+  s.misc = s.bar + NUM_BARS * 8;
   s.total = s.misc + 16;
   return s;
 }
@@ -54,6 +68,12 @@ __device__ __forceinline__ void tmem_st_1(uint32_t taddr, uint32_t v) {
 }
 __device__ __forceinline__ void tmem_st_2(uint32_t taddr, uint32_t v0, uint32_t v1) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(v0), "r"(v1)
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_tensor_l2(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
                : "memory");
 }
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -111,6 +131,21 @@ __device__ __forceinline__ void finish_token(const LinParams& p, int64_t t, int 
     *reinterpret_cast<uint32_t*>(p.os + tiled_scale_offset(t, n0 >> 5, (p.N + 127) / 128)) = word;
 }
 
+// x -> MX block of a token tile: block kb of the k-slice of row r, as TMA with a
+// 128-byte swizzle leaves it, and its scale byte.
+__device__ __forceinline__ void store_block(uint8_t* xt, uint8_t* sf, int r, int kb,
+                                            const uint32_t (&w)[16]) {
+  uint32_t o[8];
+  const uint32_t sb = quant_block32_bf16(w, o);
+  uint8_t* row = xt + r * BK;
+  const int s = r & 7;
+  *reinterpret_cast<uint4*>(row + (((2 * kb) ^ s) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(row + (((2 * kb + 1) ^ s) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+  sf[r * 16 + kb] = (uint8_t)sb;
+}
+
+// kQuant: x bf16, at most Q_ROWS rows (NT == 32) and Q_SLICES k-slices per CTA.
+template <bool kQuant>
 __global__ void __launch_bounds__(L_THREADS, 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap tmW,
                         const __grid_constant__ CUtensorMap tmX, const LinParams p) {
@@ -118,24 +153,38 @@ __global__ void __launch_bounds__(L_THREADS, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int NT = p.NT, STAGES = p.stages;
-  const Smem L = smem_layout(NT, STAGES);
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int NT = kQuant ? 32 : p.NT, STAGES = p.stages;
+  const Smem L = smem_layout(NT, STAGES, kQuant);
   const int nx = NT > 128 ? 2 : 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L.misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L.misc + 4);
-  auto bar_full = [&](int s) { return sbase + L.bar + 8u * s; };
-  auto bar_empty = [&](int s) { return sbase + L.bar + 8u * (MAX_STAGES + s); };
-  auto bar_sf = [&](int s) { return sbase + L.bar + 8u * (2 * MAX_STAGES + s); };
-  const uint32_t bar_acc = sbase + L.bar + 8u * (3 * MAX_STAGES);
-  // TMEM: NT accumulator columns, then 16 scale columns per stage
-  const uint32_t tmem_cols = NT <= 64 ? 128u : NT <= 128 ? 256u : 512u;
+  const uint32_t bars = sbase + L.bar;
+  auto bar_full = [&](int s) { return bars + 8u * s; };
+  auto bar_empty = [&](int s) { return bars + 8u * (MAX_STAGES + s); };
+  // scale segments: staged / read (shared memory), written / used up (TMEM)
+  auto bar_sfs_full = [&](int b) { return bars + 8u * (2 * MAX_STAGES + b); };
+  auto bar_sfs_free = [&](int b) { return bars + 8u * (2 * MAX_STAGES + 2 + b); };
+  auto bar_sft_ready = [&](int b) { return bars + 8u * (2 * MAX_STAGES + 4 + b); };
+  auto bar_sft_free = [&](int b) { return bars + 8u * (2 * MAX_STAGES + 6 + b); };
+  const uint32_t bar_acc = bars + 8u * (2 * MAX_STAGES + 8);
+  // TMEM: NT accumulator columns, two scale segments of SEG slices (per slice 4
+  // columns for the weights, then NT / 32 for the tokens, rounded up to 4), and
+  // with kQuant 4 columns of token scales for each of the CTA's slices
+  const int slice_cols = kQuant ? 4 : 4 + max(4, NT / 32);
+  const uint32_t x_col = NT + 2 * SEG * slice_cols;  // kQuant
+  const uint32_t tmem_cols = NT <= 128 ? 256u : 512u;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full(s), 1);
       mbar_init(bar_empty(s), 1);
-      mbar_init(bar_sf(s), SF_WARPS);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_sfs_full(b), 1);
+      mbar_init(bar_sfs_free(b), SF_WARPS);
+      mbar_init(bar_sft_ready(b), SF_WARPS);
+      mbar_init(bar_sft_free(b), 1);
     }
     mbar_init(bar_acc, 1);
     *s_abort = 0;
@@ -155,6 +204,22 @@ __global__ void __launch_bounds__(L_THREADS, 2)
   const int KT = (p.K + BK - 1) / BK;
   const int kper = (KT + p.nsplit - 1) / p.nsplit;
   const int k0 = rank * kper, k1 = min(KT, k0 + kper);  // non-empty for every rank
+  const int nsl = k1 - k0;
+  const uint8_t* sfw = p.sfw + ((int64_t)blockIdx.x * KT + k0) * 512;
+  if (warp == 0) {
+    // the first weights, while the kernel before this one still runs: they are
+    // inputs of the call, and L2 is where every writer's data meets, so asking
+    // for them early cannot leave stale bytes behind.  Two slices and the scales:
+    // all of the range took 2 us more, its requests standing before the loads'
+    if (lane < min(2, nsl)) prefetch_tensor_l2(&tmW, (k0 + lane) * BK, n0);
+    if (lane == 2) prefetch_l2_bulk(sfw, (uint32_t)nsl * 512u);
+  }
+  if (kQuant) {  // rows past M: zero payload and scales
+    uint4* z = reinterpret_cast<uint4*>(smem + L.x);
+    for (int i = threadIdx.x; i < nsl * NT * BK / 16; i += L_THREADS) z[i] = make_uint4(0, 0, 0, 0);
+    z = reinterpret_cast<uint4*>(smem + L.sfx);
+    for (int i = threadIdx.x; i < nsl * 512 / 16; i += L_THREADS) z[i] = make_uint4(0, 0, 0, 0);
+  }
   pdl_launch_dependents();
   pdl_wait();
   tc_fence_before();
@@ -162,98 +227,196 @@ __global__ void __launch_bounds__(L_THREADS, 2)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
+  // the first token of this warp in the epilogue: its residual, loaded ahead
+  const int n = n0 + 4 * lane;
+  const bool in = n < p.N;
+  const int last = (int)min((int64_t)NT, p.M - t0);
+  const int i0 = warp * p.nsplit + rank;
+  auto residual = [&](int i) {
+    return p.res && in && i < last ? *reinterpret_cast<const uint2*>(p.res + (t0 + i) * p.N + n)
+                                   : make_uint2(0, 0);
+  };
+  uint2 res = residual(i0);
+
   if (warp == 0) {
-    // ================= producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, armed_parity = 0;
-      const uint32_t bytes = (uint32_t)(W_BYTES + NT * BK + 512 + 512 * nx);
-      // the token tile's scale blocks; a block past the last token's is not read
-      const int64_t rb = t0 >> 7, last_rb = (p.M - 1) >> 7;
-      for (int kt = k0; kt < k1; ++kt) {
-        if (!wait_bar(bar_empty(stage), phase ^ 1, p.wait_limit, p.status, s_abort)) break;
-        mbar_arrive_expect_tx(bar_full(stage), bytes);
-        tma_load_2d(sbase + stage * W_BYTES, &tmW, kt * BK, n0, bar_full(stage));
-        tma_load_2d(sbase + L.x + stage * NT * BK, &tmX, kt * BK, (int)t0, bar_full(stage));
-        bulk_copy_g2s(sbase + L.sfw + stage * 512, p.sfw + ((int64_t)blockIdx.x * KT + kt) * 512,
-                      512, bar_full(stage));
-        for (int b = 0; b < nx; ++b)
-          bulk_copy_g2s(sbase + L.sfx + (stage * nx + b) * 512,
-                        p.sfx + (min(rb + b, last_rb) * KT + kt) * 512, 512, bar_full(stage));
-        armed |= 1u << stage;
-        if (phase) armed_parity |= 1u << stage; else armed_parity &= ~(1u << stage);
-        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+    // ================= producer (one elected thread issues)
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    const uint32_t bytes = kQuant ? (uint32_t)W_BYTES : (uint32_t)(W_BYTES + NT * BK);
+    // the token tile's scale blocks; a block past the last token's is not read
+    const int64_t rb = t0 >> 7, last_rb = (p.M - 1) >> 7;
+    int seg_hi = -1;  // last segment requested
+    bool ok = true;
+    auto load_segment = [&](int g) -> bool {
+      const int b = g & 1;
+      const bool got = wait_bar(bar_sfs_free(b), ((uint32_t)(g >> 1) & 1u) ^ 1u, p.wait_limit,
+                                p.status, s_abort);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      seg_hi = g;
+      if (elect_one()) {
+        const uint32_t seg_bytes = (uint32_t)min(SEG, nsl - g * SEG) * 512u;
+        mbar_arrive_expect_tx(bar_sfs_full(b), seg_bytes * (kQuant ? 1u : 1u + nx));
+        bulk_copy_g2s(sbase + L.sfw + b * SEG * 512, sfw + (int64_t)g * SEG * 512, seg_bytes,
+                      bar_sfs_full(b));
+        if (!kQuant)
+          for (int c = 0; c < nx; ++c)
+            bulk_copy_g2s(sbase + L.sfx + (b * nx + c) * SEG * 512,
+                          p.sfx + (min(rb + c, last_rb) * KT + k0 + g * SEG) * 512, seg_bytes,
+                          bar_sfs_full(b));
       }
-      // every copy this thread issued has landed before shared memory is reused
-      for (int s = 0; s < STAGES; ++s)
-        if ((armed >> s) & 1u) {
-          volatile int no_abort = 0;
-          wait_bar(bar_full(s), (armed_parity >> s) & 1u, 1ll << 32, nullptr, &no_abort);
-        }
+      __syncwarp();
+      return true;
+    };
+    ok = load_segment(0);
+    for (int it = 0; ok && it < nsl; ++it) {
+      const bool got = wait_bar(bar_empty(stage), phase ^ 1, p.wait_limit, p.status, s_abort);
+      if (!__all_sync(0xffffffffu, got)) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar_full(stage), bytes);
+        tma_load_2d(sbase + stage * W_BYTES, &tmW, (k0 + it) * BK, n0, bar_full(stage));
+        if (!kQuant)
+          tma_load_2d(sbase + L.x + stage * NT * BK, &tmX, (k0 + it) * BK, (int)t0,
+                      bar_full(stage));
+      }
+      __syncwarp();
+      armed |= 1u << stage;
+      if (phase) armed_parity |= 1u << stage; else armed_parity &= ~(1u << stage);
+      if (++stage == STAGES) { stage = 0; phase ^= 1; }
+      // the next segment's scales, half a segment ahead of its slices
+      if (it % SEG == SEG / 2 - 1 && (it / SEG + 1) * SEG < nsl) ok = load_segment(it / SEG + 1);
     }
+    // every copy this warp issued has landed before shared memory is reused
+    volatile int no_abort = 0;
+    for (int s = 0; s < STAGES; ++s)
+      if ((armed >> s) & 1u)
+        wait_bar(bar_full(s), (armed_parity >> s) & 1u, 1ll << 32, nullptr, &no_abort);
+    for (int g = max(0, seg_hi - 1); g <= seg_hi; ++g)
+      wait_bar(bar_sfs_full(g & 1), (uint32_t)(g >> 1) & 1u, 1ll << 32, nullptr, &no_abort);
     __syncwarp();
   } else if (warp == 1) {
-    // ================= MMA issuer
-    if (lane == 0) {
-      const uint32_t IDESC = make_idesc(WM, NT);
-      int stage = 0;
-      uint32_t phase = 0;
-      bool issued = false;
-      for (int kt = k0; kt < k1; ++kt) {
-        if (!wait_bar(bar_sf(stage), phase, p.wait_limit, p.status, s_abort) ||
-            !wait_bar(bar_full(stage), phase, p.wait_limit, p.status, s_abort))
-          break;
-        tc_fence_after();
-        const uint64_t adesc = make_sdesc(sbase + stage * W_BYTES, 16, 1024, 2);
-        const uint64_t bdesc = make_sdesc(sbase + L.x + stage * NT * BK, 16, 1024, 2);
-        const uint32_t t_sf = tmem + NT + 16 * stage;
+    // ================= MMA issuer (one elected thread of a converged warp)
+    const uint32_t IDESC = make_idesc(WM, NT);
+    int stage = 0, it = 0;
+    uint32_t phase = 0;
+    bool ready = false;
+    for (; it < nsl; ++it) {
+      const int g = it / SEG, i = it - g * SEG;
+      if (!__all_sync(0xffffffffu, ready)) {
+        const bool got =
+            (i != 0 || wait_bar(bar_sft_ready(g & 1), (uint32_t)(g >> 1) & 1u, p.wait_limit,
+                                p.status, s_abort)) &&
+            wait_bar(bar_full(stage), phase, p.wait_limit, p.status, s_abort);
+        if (!__all_sync(0xffffffffu, got)) break;
+      }
+      tc_fence_after();
+      // the next slice's operands, looked at before this slice's MMAs are issued
+      const int stage1 = stage + 1 == STAGES ? 0 : stage + 1;
+      ready = i != SEG - 1 && mbar_test_wait(bar_full(stage1), stage1 ? phase : phase ^ 1u);
+      const uint64_t adesc = make_sdesc(sbase + stage * W_BYTES, 16, 1024, 2);
+      const uint64_t bdesc =
+          make_sdesc(sbase + L.x + (kQuant ? it : stage) * NT * BK, 16, 1024, 2);
+      const uint32_t t_sf = tmem + NT + ((g & 1) * SEG + i) * slice_cols;
+      const uint32_t t_sfx = kQuant ? tmem + x_col + 4 * it : t_sf + 4;
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < BK / 32; ++kk)
           tc_mma_mxf8(tmem, adesc + 2 * kk, bdesc + 2 * kk,
-                      IDESC | ((uint32_t)kk << 29) | ((uint32_t)kk << 4), t_sf, t_sf + 4,
-                      ((kt - k0) | kk) != 0 ? 1u : 0u);
-        issued = true;
+                      IDESC | ((uint32_t)kk << 29) | ((uint32_t)kk << 4), t_sf, t_sfx,
+                      (it | kk) != 0 ? 1u : 0u);
         tc_commit(bar_empty(stage));
-        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        if (i == SEG - 1) tc_commit(bar_sft_free(g & 1));
+        if (it == nsl - 1) tc_commit(bar_acc);
       }
-      // this thread waits too, so no MMA is in flight when shared memory is reused
-      if (issued) {
-        tc_commit(bar_acc);
-        volatile int no_abort = 0;
-        wait_bar(bar_acc, 0, 1ll << 32, nullptr, &no_abort);
-      } else {
-        mbar_arrive(bar_acc);
-      }
+      __syncwarp();
+      if (++stage == STAGES) { stage = 0; phase ^= 1; }
     }
+    // (cut short: the MMAs issued so far are done before shared memory is reused)
+    if (it < nsl) {
+      if (elect_one()) {
+        if (it) tc_commit(bar_acc);
+        else mbar_arrive(bar_acc);
+      }
+      __syncwarp();
+    }
+    volatile int no_abort = 0;
+    wait_bar(bar_acc, 0, 1ll << 32, nullptr, &no_abort);
     __syncwarp();
   } else {
+    if (kQuant) {
+      // ================= quantizing: a warp takes slices wq and wq + 8, lane 4 r + kb
+      // block kb of rows r, r + 8, ...; two slices' loads are in flight together
+      static_assert(Q_SLICES <= 2 * DRAIN_WARPS, "slices per warp");
+      const int wq = warp - 2, kb = lane & 3;
+      for (int r0 = 0; r0 < p.M; r0 += 8) {
+        const int r = r0 + (lane >> 2);
+        uint32_t w[2][16];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int s = wq + j * DRAIN_WARPS, k = (k0 + s) * BK + 32 * kb;
+#pragma unroll
+          for (int u = 0; u < 16; ++u) w[j][u] = 0;
+          if (s < nsl && r < p.M && k < p.K) {
+            const uint16_t* src = p.x + (int64_t)r * p.K + k;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (u < 2 || k + 16 < p.K) {  // (K % 32 == 16: a last block of 16)
+                const uint4 v = ld_nc_v4(src + 8 * u);
+                w[j][4 * u] = v.x; w[j][4 * u + 1] = v.y; w[j][4 * u + 2] = v.z; w[j][4 * u + 3] = v.w;
+              }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int s = wq + j * DRAIN_WARPS;
+          if (s < nsl && r < p.M)
+            store_block(smem + L.x + s * NT * BK, smem + L.sfx + s * 512, r, kb, w[j]);
+        }
+      }
+      fence_proxy_async_smem();  // the MMAs read the tiles through the async proxy
+      // (no wait precedes it in these warps: every one of them arrives)
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * DRAIN_WARPS) : "memory");
+    }
     if (warp < 2 + SF_WARPS) {
-      // ================= scale-factor writers: 4 columns of weight scales, NT / 32
-      // columns of token scales per stage (32-row groups g0 .. of their 128-row block)
-      const uint32_t t_q = tmem + ((uint32_t)((warp & 3) * 32) << 16) + NT;
+      // ================= scale-factor writers: per slice 4 columns of weight scales, and
+      // NT / 32 columns of token scales (32-row groups g0 .. of their 128-row block)
+      const uint32_t t_q = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      if (kQuant)
+        for (int s = 0; s < nsl; ++s)
+          tmem_st_1(t_q + x_col + 4 * s,
+                    *reinterpret_cast<const uint32_t*>(smem + L.sfx + s * 512 + lane * 16));
       const int g0 = (int)(t0 & 127) >> 5;
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int kt = k0; kt < k1; ++kt) {
-        const bool got = wait_bar(bar_full(stage), phase, p.wait_limit, p.status, s_abort);
+      for (int g = 0; g * SEG < nsl; ++g) {
+        const int b = g & 1;
+        const uint32_t par = (uint32_t)(g >> 1) & 1u;
+        const bool got =
+            wait_bar(bar_sfs_full(b), par, p.wait_limit, p.status, s_abort) &&
+            wait_bar(bar_sft_free(b), par ^ 1u, p.wait_limit, p.status, s_abort);
         if (!__all_sync(0xffffffffu, got)) break;
-        const uint32_t col = t_q + 16 * stage;
-        tmem_st_4(col, *reinterpret_cast<const uint4*>(smem + L.sfw + stage * 512 + lane * 16));
-        const uint8_t* sx = smem + L.sfx + stage * nx * 512 + lane * 16;
-        if (NT == 32) {
-          tmem_st_1(col + 4, *reinterpret_cast<const uint32_t*>(sx + 4 * g0));
-        } else if (NT == 64) {
-          const uint2 w = *reinterpret_cast<const uint2*>(sx + 4 * g0);
-          tmem_st_2(col + 4, w.x, w.y);
-        } else {
-          tmem_st_4(col + 4, *reinterpret_cast<const uint4*>(sx));
-          if (NT == 256) tmem_st_4(col + 8, *reinterpret_cast<const uint4*>(sx + 512));
+        const int len = min(SEG, nsl - g * SEG);
+        const uint8_t* sw = smem + L.sfw + b * SEG * 512 + lane * 16;
+        const uint8_t* sx = smem + L.sfx + b * nx * SEG * 512 + lane * 16;
+        for (int i = 0; i < len; ++i) {
+          const uint32_t col = t_q + NT + (b * SEG + i) * slice_cols;
+          tmem_st_4(col, *reinterpret_cast<const uint4*>(sw + i * 512));
+          if (kQuant) continue;
+          if (NT == 32) {
+            tmem_st_1(col + 4, *reinterpret_cast<const uint32_t*>(sx + i * 512 + 4 * g0));
+          } else if (NT == 64) {
+            const uint2 w = *reinterpret_cast<const uint2*>(sx + i * 512 + 4 * g0);
+            tmem_st_2(col + 4, w.x, w.y);
+          } else {
+            tmem_st_4(col + 4, *reinterpret_cast<const uint4*>(sx + i * 512));
+            if (NT == 256)
+              tmem_st_4(col + 8, *reinterpret_cast<const uint4*>(sx + (SEG + i) * 512));
+          }
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_sf(stage));
-        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        if (lane == 0) {
+          mbar_arrive(bar_sft_ready(b));
+          mbar_arrive(bar_sfs_free(b));
+        }
       }
     }
     // ================= accumulator -> shared memory [token][128], over the stages
@@ -264,7 +427,7 @@ __global__ void __launch_bounds__(L_THREADS, 2)
       tc_fence_after();
       float* buf = reinterpret_cast<float*>(smem);
       const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16);
-      const int cols = NT / 2, last = (int)min((int64_t)NT, p.M - t0);
+      const int cols = NT / 2;
       for (int c = half * cols; c < (half + 1) * cols && c < last; c += 16) {
         uint32_t v[16];
         tmem_ld_16(t_row + c, v);
@@ -280,8 +443,6 @@ __global__ void __launch_bounds__(L_THREADS, 2)
 
   // ================= epilogue: a warp per token of this CTA's share
   {
-    const int n = n0 + 4 * lane;
-    const bool in = n < p.N;
     float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.bias && in) {
       if (p.bias32) {
@@ -292,21 +453,22 @@ __global__ void __launch_bounds__(L_THREADS, 2)
                            bf16_bits_to_float(b.y & 0xFFFFu), bf16_bits_to_float(b.y >> 16));
       }
     }
-    const int last = (int)min((int64_t)NT, p.M - t0);
-    for (int i = warp * p.nsplit + rank; i < last; i += WARPS * p.nsplit) {
-      uint2 res = make_uint2(0, 0);
-      if (p.res && in) res = *reinterpret_cast<const uint2*>(p.res + (t0 + i) * p.N + n);
+    for (int i = i0; i < last; i += WARPS * p.nsplit) {
+      const uint2 res_next = residual(i + WARPS * p.nsplit);
       const uint32_t at = sbase + (uint32_t)(i * WM + 4 * lane) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (p.nsplit == 1) {
         v = *reinterpret_cast<const float4*>(smem + (i * WM + 4 * lane) * 4);
       } else {
-        for (int r = 0; r < p.nsplit; ++r) {  // split order, whichever CTA adds
-          const float4 u = ld_cluster_f4(mapa_cluster(at, r));
-          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-        }
+#pragma unroll
+        for (int r = 0; r < MAX_SPLIT; ++r)  // split order, whichever CTA adds
+          if (r < p.nsplit) {
+            const float4 u = ld_cluster_f4(mapa_cluster(at, r));
+            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+          }
       }
       finish_token(p, t0 + i, n0, lane, v, bias, res);
+      res = res_next;
     }
   }
 
@@ -329,7 +491,7 @@ struct Plan {
 static Plan make_plan(int64_t M, int N, int K) {
   Plan pl;
   pl.NT = M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-  pl.stages = pl.NT <= 32 ? 5 : pl.NT <= 64 ? 4 : pl.NT <= 128 ? 6 : 4;
+  pl.stages = pl.NT <= 32 ? 4 : pl.NT <= 64 ? 3 : pl.NT <= 128 ? 5 : 4;
   const int64_t slots = (int64_t)num_sms() * (pl.NT <= 64 ? 2 : 1);
   const int64_t tiles = ceil_div(N, WM) * ceil_div(M, pl.NT);
   const int KT = (int)ceil_div(K, BK);
@@ -340,14 +502,9 @@ static Plan make_plan(int64_t M, int N, int K) {
   return pl;
 }
 
-}  // namespace linear
-
-cudaError_t launch_linear_fused(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq,
-                                const uint8_t* ws, int64_t M, int N, int K, const void* bias,
-                                bool bias32, int act, const uint16_t* residual, uint16_t* out,
-                                uint8_t* oq, uint8_t* os, cudaStream_t stream) {
-  using namespace linear;
-  if (M == 0) return cudaSuccess;
+template <bool kQuant>
+static cudaError_t launch_split(const uint8_t* xq, const uint8_t* wq, LinParams p,
+                                cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -355,35 +512,16 @@ cudaError_t launch_linear_fused(const uint8_t* xq, const uint8_t* xs, const uint
   const uint64_t ctx = context_id();
   if (ctx == 0 || configured[dev] != ctx) {
     const cudaError_t err = cudaFuncSetAttribute(
-        linear_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+        linear_split_kernel<kQuant>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
     if (err != cudaSuccess) return err;
     configured[dev] = context_id();
   }
-  LinParams p = {};
-  p.sfw = ws;
-  p.sfx = xs;
-  p.bias = bias;
-  p.res = residual;
-  p.out = out;
-  p.oq = oq;
-  p.os = os;
-  p.M = M;
-  p.N = N;
-  p.K = K;
-  p.act = act;
-  p.bias32 = bias32;
-  p.status = device_status_ptr();
-  p.wait_limit = wait_limit_cycles();
-  if (M > 256) {
-    int bn = 0;
-    pair_cycles(M, N, K, &bn);
-    const cudaError_t err = launch_pair(xq, wq, p, bn, stream);
-    if (err != cudaErrorNotSupported) return err;
-  }
-  const Plan pl = make_plan(M, N, K);
+  Plan pl = make_plan(p.M, p.N, p.K);
+  if (kQuant) pl.stages = 3;
   CUtensorMap tmW, tmX;
-  if (!make_map(&tmW, wq, (uint64_t)K, (uint64_t)N, BK, WM) ||
-      !make_map(&tmX, xq, (uint64_t)K, (uint64_t)M, BK, (uint32_t)pl.NT))
+  if (!make_map(&tmW, wq, (uint64_t)p.K, (uint64_t)p.N, BK, WM)) return cudaErrorInvalidValue;
+  if (kQuant) tmX = tmW;  // not read
+  else if (!make_map(&tmX, xq, (uint64_t)p.K, (uint64_t)p.M, BK, (uint32_t)pl.NT))
     return cudaErrorInvalidValue;
   p.NT = pl.NT;
   p.stages = pl.stages;
@@ -398,11 +536,61 @@ cudaError_t launch_linear_fused(const uint8_t* xq, const uint8_t* xs, const uint
   attr[1].val.clusterDim.z = (unsigned)pl.nsplit;
   cfg.attrs = attr;
   cfg.numAttrs = pl.nsplit > 1 ? 2 : 1;
-  cfg.gridDim = dim3((unsigned)ceil_div(N, WM), (unsigned)ceil_div(M, pl.NT), (unsigned)pl.nsplit);
+  cfg.gridDim =
+      dim3((unsigned)ceil_div(p.N, WM), (unsigned)ceil_div(p.M, pl.NT), (unsigned)pl.nsplit);
   cfg.blockDim = dim3(L_THREADS);
-  cfg.dynamicSmemBytes = (size_t)smem_layout(pl.NT, pl.stages).total + 1024;
+  cfg.dynamicSmemBytes = (size_t)smem_layout(pl.NT, pl.stages, kQuant).total + 1024;
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, linear_split_kernel, tmW, tmX, p);
+  return cudaLaunchKernelEx(&cfg, linear_split_kernel<kQuant>, tmW, tmX, p);
+}
+
+}  // namespace linear
+
+// bf16 rows are quantized in the product's kernel while a CTA has little to do
+// for it: at most 96 rows x k-slices.  Measured against a quantizing kernel and
+// the product (us, graph replay; the host's call is 3 us shorter besides): 4096
+// columns, K 12288 (12 slices a CTA): 11.8 / 12.9 at 1 row, 13.6 / 13.4 at 8, 16.0 /
+// 14.0 at 16; K 4096 (4 slices): 6.3 / 7.3 at 8 rows, 7.4 / 7.7 at 16, 9.2 / 8.2 at 32.
+bool linear_quantizes_in_place(int64_t M, int N, int K) {
+  if (M > linear::Q_ROWS) return false;
+  const linear::Plan pl = linear::make_plan(M, N, K);
+  const int64_t kper = ceil_div(ceil_div(K, linear::BK), pl.nsplit);
+  return kper <= linear::Q_SLICES && M * kper <= 96;
+}
+
+cudaError_t launch_linear_fused(const uint16_t* x, const uint8_t* xq, const uint8_t* xs,
+                                const uint8_t* wq, const uint8_t* ws, int64_t M, int N, int K,
+                                const void* bias, bool bias32, int act, const uint16_t* residual,
+                                uint16_t* out, uint8_t* oq, uint8_t* os, cudaStream_t stream) {
+  using namespace linear;
+  if (M == 0) return cudaSuccess;
+  LinParams p = {};
+  p.x = x;
+  p.sfw = ws;
+  p.sfx = xs;
+  p.bias = bias;
+  p.res = residual;
+  p.out = out;
+  p.oq = oq;
+  p.os = os;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.act = act;
+  p.bias32 = bias32;
+  p.status = device_status_ptr();
+  p.wait_limit = wait_limit_cycles();
+  if (x) {
+    if (!linear_quantizes_in_place(M, N, K)) return cudaErrorInvalidValue;
+    return launch_split<true>(nullptr, wq, p, stream);
+  }
+  if (M > 256) {
+    int bn = 0;
+    pair_cycles(M, N, K, &bn);
+    const cudaError_t err = launch_pair(xq, wq, p, bn, stream);
+    if (err != cudaErrorNotSupported) return err;
+  }
+  return launch_split<false>(xq, wq, p, stream);
 }
 
 }  // namespace mxmoe

@@ -10,6 +10,7 @@ namespace linear {
 using namespace gemm;
 
 struct LinParams {
+  const uint16_t* x;       // [M, K] bf16 (split kernel that quantizes in place)
   const uint8_t* sfw;      // weight scales, MMA layout [ceil(N/128)][KT] chunks
   const uint8_t* sfx;      // activation scales, MMA layout
   const void* bias;        // [N] or null

@@ -50,6 +50,8 @@ __global__ void __launch_bounds__(256) mx_quantize_rows_kernel(const uint16_t* _
                                                                uint8_t* __restrict__ q,
                                                                uint8_t* __restrict__ scale,
                                                                int64_t* __restrict__ offsets) {
+  pdl_launch_dependents();
+  pdl_wait();
   if (offsets && blockIdx.x == 0 && threadIdx.x == 0) {
     offsets[0] = 0;
     offsets[1] = rows;
@@ -112,13 +114,10 @@ static cudaError_t launch_rows(const uint16_t* x, int64_t rows, int64_t K, uint8
   int64_t blocks = ceil_div(n, 256);
   const int64_t cap = (int64_t)num_sms() * 8;
   if (blocks > cap) blocks = cap;
-  if (((uintptr_t)x & 31u) == 0)
-    mx_quantize_rows_kernel<true, kTiled, kFp4>
-        <<<(unsigned)blocks, 256, 0, stream>>>(x, rows, K, q, scale, offsets);
-  else
-    mx_quantize_rows_kernel<false, kTiled, kFp4>
-        <<<(unsigned)blocks, 256, 0, stream>>>(x, rows, K, q, scale, offsets);
-  return cudaGetLastError();
+  auto kern = ((uintptr_t)x & 31u) == 0 ? mx_quantize_rows_kernel<true, kTiled, kFp4>
+                                        : mx_quantize_rows_kernel<false, kTiled, kFp4>;
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, stream, x, rows, K, q, scale,
+                    offsets);
 }
 
 cudaError_t launch_mx_quantize_tiled(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q,

@@ -116,8 +116,8 @@ def _linear(lib, **kw):
     (dict(xq=P, xs=P), 4), (dict(wq=NUL), 1), (dict(ws=NUL), 1), (dict(x=NUL), 1),
     (dict(x=NUL, xq=P), 1), (dict(out=NUL, residual=NUL), 1),
     (dict(out=NUL, residual=NUL, oq=P), 1), (dict(x=ODD), 2), (dict(wq=ODD), 2),
-    (dict(bias=ODD), 2), (dict(residual=ODD), 2), (dict(out=ODD), 2), (dict(ws_=NUL), 5),
-    (dict(ws_bytes=256), 5), (dict(ws_=P16), 2), (dict(M=0, x=NUL, wq=NUL, ws_=NUL), 0)])
+    (dict(bias=ODD), 2), (dict(residual=ODD), 2), (dict(out=ODD), 2), (dict(M=33, ws_=NUL), 5),
+    (dict(M=33, ws_bytes=256), 5), (dict(M=33, ws_=P16), 2), (dict(M=0, x=NUL, wq=NUL, ws_=NUL), 0)])
 def test_linear_refusals(lib, kw, code):
     assert _linear(lib, **kw) == code
 
@@ -140,9 +140,12 @@ def test_balance_refusals(lib, kw, code):
 
 
 def test_workspace_sizes(lib):
-    assert lib.mxfp8_linear_fused_workspace_size(200, 336) >= 200 * 336 + 2 * 3 * 512
-    assert lib.mxfp8_linear_fused_workspace_size(8, 40) == 0
-    assert lib.mxfp8_linear_fused_workspace_size(-1, 64) == 0
+    assert lib.mxfp8_linear_fused_workspace_size(200, 64, 336) >= 200 * 336 + 2 * 3 * 512
+    assert lib.mxfp8_linear_fused_workspace_size(100, 64, 40) == 0
+    # few rows and a K range that fits are quantized in the product's kernel
+    assert lib.mxfp8_linear_fused_workspace_size(8, 64, 64) == 0
+    assert lib.mxfp8_linear_fused_workspace_size(33, 64, 64) > 0
+    assert lib.mxfp8_linear_fused_workspace_size(-1, 64, 64) == 0
     assert lib.moe_balance_loss_workspace_size(16384, 128) >= 128 * 4
     assert lib.moe_balance_loss_workspace_size(4, 2000) == 0
     # one kernel without a workspace up to 1024 tokens
