@@ -18,24 +18,32 @@ from .api import _need, _u8, mx_quantize_3d, mx_scales_to_mma_layout
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
-def _stream(t):
-    """The current stream of the tensor's device, as an integer handle."""
-    return torch.cuda.current_stream(t.device).cuda_stream
+_BF16, _F32, _U8, _I64 = torch.bfloat16, torch.float32, torch.uint8, torch.int64
+_empty = torch.empty
+# The current stream's handle by device index: torch.cuda.current_stream without the
+# Stream object, which takes longer than a launch.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows(t, name, dtypes, aligned=False):
-    """A CUDA tensor of one of ``dtypes``, contiguous."""
+def _bad(t, name, dtypes):
+    """What is wrong with a tensor that is not on CUDA, contiguous and of one of dtypes."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-_HALF_OR_FLOAT = (torch.bfloat16, torch.float32)
+def _rows(t, name, dtypes):
+    """A CUDA tensor of one of ``dtypes``, contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes
+            and t.is_contiguous()):
+        _bad(t, name, dtypes)
+
+
+_HALF_OR_FLOAT = (_BF16, _F32)
 
 
 def _mma_scale_shape(M: int, K: int):
@@ -54,21 +62,22 @@ def mx_add_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, bf16_out: 
     residual's type; pass ``residual_out=residual`` to update it in place)."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise TypeError("x must be a torch.Tensor of at least one dimension")
-    H = x.shape[-1]
-    ldx = H
-    if x.dim() == 2 and x.stride(1) == 1 and x.is_cuda and x.dtype == torch.bfloat16:
-        ldx = x.stride(0) if x.shape[0] > 1 else H
+    shape = x.shape
+    H = ldx = shape[-1]
+    if x.is_cuda and x.dtype is _BF16 and len(shape) == 2 and x.stride(1) == 1:
+        if shape[0] > 1:
+            ldx = x.stride(0)
+            if ldx < H:
+                raise ValueError("x: overlapping rows")
     else:
-        _rows(x, "x", (torch.bfloat16,))
-    if ldx < H:
-        raise ValueError("x: overlapping rows")
+        _rows(x, "x", (_BF16,))
     _rows(weight, "weight", _HALF_OR_FLOAT)
-    if weight.dim() != 1 or weight.shape[0] != H:
+    if weight.shape != (H,):
         raise ValueError(f"weight is {tuple(weight.shape)}, x has H = {H}")
-    dev, shape = x.device, x.shape
+    dev = x.device
     M = x.numel() // H if H else 0
-    out = {}
-    res_ptr = res_out_ptr = None
+    res_ptr = res_out_ptr = y_ptr = None
+    res32 = 0
     if residual is not None:
         _rows(residual, "residual", _HALF_OR_FLOAT)
         if residual.shape != shape:
@@ -79,22 +88,22 @@ def mx_add_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, bf16_out: 
             _rows(residual_out, "residual_out", (residual.dtype,))
             if residual_out.shape != shape:
                 raise ValueError(f"residual_out is {tuple(residual_out.shape)}, x is {tuple(shape)}")
+        res32 = residual.dtype is _F32
         res_ptr, res_out_ptr = residual.data_ptr(), residual_out.data_ptr()
-        out["residual"] = residual_out
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    q = torch.empty(shape, dtype=torch.uint8, device=dev)
-    s = torch.empty(_mma_scale_shape(M, H) if mma_scales else shape[:-1] + (-(-H // 32),),
-                    dtype=torch.uint8, device=dev)
-    out["q"], out["s"] = q, s
-    y_ptr = None
+    q = _empty(shape, dtype=_U8, device=dev)
+    s = _empty(_mma_scale_shape(M, H) if mma_scales else (*shape[:-1], -(-H // 32)), dtype=_U8,
+               device=dev)
+    out = {"q": q, "s": s}
+    if residual is not None:
+        out["residual"] = residual_out
     if bf16_out:
-        out["y"] = y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out["y"] = y = _empty(shape, dtype=_BF16, device=dev)
         y_ptr = y.data_ptr()
     rc = _lib.load().mx_add_rmsnorm_quant(
-        x.data_ptr(), ldx, res_ptr, residual is not None and residual.dtype == torch.float32,
-        res_out_ptr, weight.data_ptr(), weight.dtype == torch.float32, eps, M, H, y_ptr,
-        q.data_ptr(), s.data_ptr(), mma_scales, _stream(x))
+        x.data_ptr(), ldx, res_ptr, res32, res_out_ptr, weight.data_ptr(), weight.dtype is _F32,
+        eps, M, H, y_ptr, q.data_ptr(), s.data_ptr(), mma_scales, _raw_stream(dev.index))
     if rc:
         _lib.check("mx_add_rmsnorm_quant", rc)
     return out
@@ -113,75 +122,89 @@ def mxfp8_linear_fused(x, wq, ws_mma, bias=None, act=None, residual=None, mx_out
     tensor-core layout; bias bf16 or fp32 [N]; act one of "none", "relu",
     "gelu", "gelu_tanh", "silu"; residual bf16 [.., N].  Returns bf16 [.., N],
     or with ``mx_out`` the MXFP8 pair of act(..) (no residual)."""
-    xq = xs = x_ptr = xq_ptr = xs_ptr = ws_ptr = None
-    ws_bytes = 0
-    if isinstance(x, tuple):
-        xq, xs = x
-        xq = _u8(xq)
-        _rows(xq, "x[0]", (torch.uint8,))
-        _rows(xs, "x[1]", (torch.uint8,))
-        xin = xq
-    else:
-        _rows(x, "x", (torch.bfloat16,))
-        xin = x
     wq = _u8(wq)
-    _need(wq, "wq", torch.uint8, 2)
-    _rows(ws_mma, "ws_mma", (torch.uint8,))
+    _need(wq, "wq", _U8, 2)
+    _check_weight(wq, ws_mma, bias, act)
+    return _fused(x, wq, ws_mma, bias, ACTIVATIONS[act], residual, mx_out, out, workspace)
+
+
+def _check_weight(wq, ws_mma, bias, act):
     N, K = wq.shape
-    if xin.dim() < 1 or xin.shape[-1] != K:
-        raise ValueError(f"wq is {tuple(wq.shape)}, x is {tuple(xin.shape)}")
-    M = xin.numel() // K if K else 0
-    if ws_mma.numel() != _mma_scale_shape(N, K)[0] * _mma_scale_shape(N, K)[1]:
+    _rows(ws_mma, "ws_mma", (_U8,))
+    rows, cols = _mma_scale_shape(N, K)
+    if ws_mma.numel() != rows * cols:
         raise ValueError("ws_mma is not in the tensor-core layout of wq's scales")
-    if xq is not None:
-        if xs.numel() != _mma_scale_shape(M, K)[0] * _mma_scale_shape(M, K)[1]:
-            raise ValueError("x's scales are not in the tensor-core layout")
-        xq_ptr, xs_ptr = xq.data_ptr(), xs.data_ptr()
-    else:
-        x_ptr = x.data_ptr()
-        need = mxfp8_linear_fused_workspace_size(M, N, K)
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        if need:
-            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if act not in ACTIVATIONS:
         raise ValueError(f"act: expected one of {sorted(k for k in ACTIVATIONS if k)}, got {act!r}")
-    bias_ptr, bias32 = None, 0
     if bias is not None:
         _rows(bias, "bias", _HALF_OR_FLOAT)
-        if bias.dim() != 1 or bias.shape[0] != N:
+        if bias.shape != (N,):
             raise ValueError(f"bias is {tuple(bias.shape)}, wq has N = {N}")
-        bias_ptr, bias32 = bias.data_ptr(), bias.dtype == torch.float32
-    shape = xin.shape[:-1] + (N,)
-    res_ptr = None
+
+
+def _fused(x, wq, ws_mma, bias, act, residual, mx_out, out, workspace):
+    """mxfp8_linear_fused on a checked weight.  workspace: a tensor, None, or a
+    function of (M, device) that gives one (or None) for bf16 input."""
+    N, K = wq.shape
+    x_ptr = xq_ptr = xs_ptr = ws_ptr = res_ptr = out_ptr = oq_ptr = os_ptr = None
+    ws_bytes = 0
+    lib = _lib.load()
+    if type(x) is tuple:
+        xin, xs = x
+        xin = _u8(xin)
+        _rows(xin, "x[0]", (_U8,))
+        _rows(xs, "x[1]", (_U8,))
+    else:
+        xin, xs = x, None
+        _rows(x, "x", (_BF16,))
+    shape = xin.shape
+    if not shape or shape[-1] != K:
+        raise ValueError(f"wq is {tuple(wq.shape)}, x is {tuple(shape)}")
+    M = xin.numel() // K if K else 0
+    dev = xin.device
+    if xs is not None:
+        rows, cols = _mma_scale_shape(M, K)
+        if xs.numel() != rows * cols:
+            raise ValueError("x's scales are not in the tensor-core layout")
+        xq_ptr, xs_ptr = xin.data_ptr(), xs.data_ptr()
+    else:
+        x_ptr = x.data_ptr()
+        if workspace is None:
+            need = lib.mxfp8_linear_fused_workspace_size(M, N, K)
+            workspace = _empty(need, dtype=_U8, device=dev) if need else None
+        elif callable(workspace):
+            workspace = workspace(M, dev)
+        if workspace is not None:
+            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    shape = (M, N) if len(shape) == 2 else (*shape[:-1], N)
     if residual is not None:
         if mx_out:
             raise ValueError("an MXFP8 result takes no residual")
-        _rows(residual, "residual", (torch.bfloat16,))
+        _rows(residual, "residual", (_BF16,))
         if residual.shape != shape:
-            raise ValueError(f"residual is {tuple(residual.shape)}, the result {tuple(shape)}")
+            raise ValueError(f"residual is {tuple(residual.shape)}, the result {shape}")
         res_ptr = residual.data_ptr()
-    out_ptr = oq_ptr = os_ptr = None
     if mx_out:
         if out is not None:
             raise ValueError("out holds a bf16 result")
-        oq = torch.empty(shape, dtype=torch.uint8, device=xin.device)
-        os_ = torch.empty(_mma_scale_shape(M, N), dtype=torch.uint8, device=xin.device)
-        oq_ptr, os_ptr = oq.data_ptr(), os_.data_ptr()
+        out = (_empty(shape, dtype=_U8, device=dev),
+               _empty(_mma_scale_shape(M, N), dtype=_U8, device=dev))
+        oq_ptr, os_ptr = out[0].data_ptr(), out[1].data_ptr()
     else:
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=xin.device)
+            out = _empty(shape, dtype=_BF16, device=dev)
         else:
-            _rows(out, "out", (torch.bfloat16,))
+            _rows(out, "out", (_BF16,))
             if out.shape != shape:
-                raise ValueError(f"out is {tuple(out.shape)}, the result {tuple(shape)}")
+                raise ValueError(f"out is {tuple(out.shape)}, the result {shape}")
         out_ptr = out.data_ptr()
-    rc = _lib.load().mxfp8_linear_fused(
-        x_ptr, xq_ptr, xs_ptr, wq.data_ptr(), ws_mma.data_ptr(), M, N, K, bias_ptr, bias32,
-        ACTIVATIONS[act], res_ptr, out_ptr, oq_ptr, os_ptr, ws_ptr, ws_bytes, _stream(xin))
+    bias_ptr, bias32 = (None, 0) if bias is None else (bias.data_ptr(), bias.dtype is _F32)
+    rc = lib.mxfp8_linear_fused(
+        x_ptr, xq_ptr, xs_ptr, wq.data_ptr(), ws_mma.data_ptr(), M, N, K, bias_ptr, bias32, act,
+        res_ptr, out_ptr, oq_ptr, os_ptr, ws_ptr, ws_bytes, _raw_stream(dev.index))
     if rc:
         _lib.check("mxfp8_linear_fused", rc)
-    return (oq, os_) if mx_out else out
+    return out
 
 
 class MXFP8FusedLinear:
@@ -196,24 +219,28 @@ class MXFP8FusedLinear:
         self.N, self.K = self.wq.shape
         self.ws_mma = mx_scales_to_mma_layout(ws, self.K)
         self.bias, self.act = bias, act
+        _need(self.wq, "wq", _U8, 2)
+        _check_weight(self.wq, self.ws_mma, bias, act)
         self._ws = None
+        self._need = {}  # rows -> workspace bytes
 
     @classmethod
     def from_bf16(cls, w, bias=None, act=None):
         return cls(*mx_quantize_3d(w), bias=bias, act=act)
 
     def workspace(self, M: int, device):
-        need = mxfp8_linear_fused_workspace_size(M, self.N, self.K)
-        if need and (self._ws is None or self._ws.numel() < need):
-            self._ws = torch.empty(need, dtype=torch.uint8, device=device)
+        need = self._need.get(M)
+        if need is None:
+            need = self._need[M] = mxfp8_linear_fused_workspace_size(M, self.N, self.K)
+        if not need:
+            return None
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = _empty(need, dtype=_U8, device=device)
         return self._ws
 
     def __call__(self, x, residual=None, mx_out: bool = False, out=None):
-        ws = None
-        if not isinstance(x, tuple) and x.is_cuda:
-            ws = self.workspace(x.numel() // self.K, x.device)
-        return mxfp8_linear_fused(x, self.wq, self.ws_mma, self.bias, self.act, residual, mx_out,
-                                  out, ws)
+        return _fused(x, self.wq, self.ws_mma, self.bias, ACTIVATIONS[self.act], residual, mx_out,
+                      out, self.workspace)
 
 
 def moe_balance_loss_workspace_size(T: int, E: int) -> int:
@@ -227,16 +254,17 @@ _BALANCE_ONE_KERNEL = 1024
 def _balance(logits, topk_ids, mask, counts, coef, grad):
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor (the library has no CPU path)")
-    if logits.dtype != torch.float32 or logits.dim() != 2:
+    shape = logits.shape
+    if logits.dtype is not _F32 or len(shape) != 2:
         raise TypeError("logits: expected fp32 [T, E]")
-    T, E = logits.shape
+    T, E = shape
     if E > 1 and logits.stride(1) != 1:
         raise ValueError("logits: a row must be contiguous")
     ldl = logits.stride(0) if T > 1 else E
     if ldl < E:
         raise ValueError("logits: overlapping rows")
-    _need(topk_ids, "topk_ids", torch.int32, 2)
-    if topk_ids.shape[0] != T:
+    _rows(topk_ids, "topk_ids", (torch.int32,))
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
         raise ValueError("logits and topk_ids disagree on T")
     mask_ptr = counts_ptr = grad_ptr = None
     if mask is not None:
@@ -245,24 +273,27 @@ def _balance(logits, topk_ids, mask, counts, coef, grad):
             raise ValueError(f"mask is {tuple(mask.shape)}, logits have T = {T}")
         mask_ptr = mask.data_ptr()
     if counts is not None:
-        _rows(counts, "counts", (torch.int64,))
+        _rows(counts, "counts", (_I64,))
         if counts.shape != (E,):
             raise ValueError(f"counts is {tuple(counts.shape)}, logits have E = {E}")
         counts_ptr = counts.data_ptr()
     dev = logits.device
     lib = _lib.load()
-    need = 0 if T <= _BALANCE_ONE_KERNEL else lib.moe_balance_loss_workspace_size(T, E)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    own_counts = torch.empty(E, dtype=torch.int64, device=dev)
+    ws_ptr, need = None, 0
+    if T > _BALANCE_ONE_KERNEL:
+        need = lib.moe_balance_loss_workspace_size(T, E)
+        ws = _empty(need, dtype=_U8, device=dev)
+        ws_ptr = ws.data_ptr()
+    loss = _empty((), dtype=_F32, device=dev)
+    own_counts = _empty(E, dtype=_I64, device=dev)
     out = {"loss": loss, "counts": own_counts}
     if grad:
-        out["dlogits"] = d = torch.empty((T, E), dtype=torch.float32, device=dev)
+        out["dlogits"] = d = _empty(shape, dtype=_F32, device=dev)
         grad_ptr = d.data_ptr()
     rc = lib.moe_balance_loss(
         logits.data_ptr(), ldl, topk_ids.data_ptr(), mask_ptr, counts_ptr, T, E,
-        topk_ids.shape[1], coef, loss.data_ptr(), own_counts.data_ptr(), grad_ptr,
-        ws.data_ptr() if need else None, need, _stream(logits))
+        topk_ids.shape[1], coef, loss.data_ptr(), own_counts.data_ptr(), grad_ptr, ws_ptr, need,
+        _raw_stream(dev.index))
     if rc:
         _lib.check("moe_balance_loss", rc)
     return out

@@ -483,27 +483,65 @@ __global__ void __launch_bounds__(L_THREADS, 2)
   }
 }
 
-// Tile and split choice: the token tile covers the batch up to 256 tokens;
-// K is split until the CTAs fill the GPU (two fit on an SM up to 64 tokens).
+// Kernel and tile choice by estimated time, microseconds, from a sweep of 33 to 1024
+// rows over six products (400 x 336 up to 12288 x 4096) on GB300, where the choice
+// was the best of the sweep or within 15% of it.
+//   split kernel: launch and tail 3.1 (0.6 and 1.0 more at NT = 128 and 256), a
+//     cluster's exchange 1.4, 0.032 per token that a CTA finishes, and per k-slice 0.27 / 0.30 / 0.34 / 0.62 at NT = 32 / 64 / 128 /
+//     256 (a third more where two CTAs share an SM), times the CTA waves;
+//   pair kernel: 3.4, 0.0095 per tile column (the last tile's epilogue), and per
+//     k-slice and round of tiles 0.20 / 0.225 / 0.255 at BN = 128 / 192 / 224.
+// (200 rows, 4096 x 12288: split 256 / 4 19.2 us, pair 23.8; 400 rows: 28.9 and 24.6.)
 struct Plan {
+  int bn;  // pair kernel's tile width, 0 for the split kernel
   int NT, stages, nsplit;
 };
 static Plan make_plan(int64_t M, int N, int K) {
-  Plan pl;
-  pl.NT = M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-  pl.stages = pl.NT <= 32 ? 4 : pl.NT <= 64 ? 3 : pl.NT <= 128 ? 5 : 4;
-  const int64_t slots = (int64_t)num_sms() * (pl.NT <= 64 ? 2 : 1);
-  const int64_t tiles = ceil_div(N, WM) * ceil_div(M, pl.NT);
+  const int sms = num_sms();
   const int KT = (int)ceil_div(K, BK);
-  int s = (int)std::min<int64_t>({slots / tiles, (int64_t)KT, (int64_t)MAX_SPLIT});
-  if (s < 1) s = 1;
-  const int kper = (int)ceil_div(KT, s);
-  pl.nsplit = (int)ceil_div(KT, kper);  // no empty range
-  return pl;
+  const int64_t tiles_w = ceil_div(N, WM);
+  Plan best = {};
+  double best_t = 0;
+  for (int nt : {32, 64, 128, 256}) {
+    if (nt > 32 && nt >= 2 * M) break;  // the tile before it holds every row
+    const int64_t tiles = tiles_w * ceil_div(M, nt);
+    const int slots = sms * (nt <= 64 ? 2 : 1);
+    const double slice = nt == 32 ? 0.27 : nt == 64 ? 0.30 : nt == 128 ? 0.34 : 0.62;
+    for (int s = 1; s <= std::min(MAX_SPLIT, KT); ++s) {
+      const int kper = (int)ceil_div(KT, s);
+      if ((int)ceil_div(KT, kper) != s) continue;  // an empty range
+      const int64_t ctas = tiles * s;
+      // clusters in one wave only (second waves of clusters start late: 200 rows,
+      // 4096 x 12288 in clusters of 7 took 52 us), and of sizes that pack: on 152 SMs
+      // 144 can hold clusters of 4 and 120 clusters of 8
+      if (s == 5 || s == 7 || (s > 1 && ctas > slots * (s > 4 ? 0.9 : s > 2 ? 0.95 : 1.0))) continue;
+      const double waves = (double)ceil_div(ctas, slots);
+      const double shared = ctas > sms && nt <= 64 ? 1.35 : 1.0;
+      const double t = 3.1 + (nt == 128 ? 0.6 : nt == 256 ? 1.0 : 0.0) + (s > 1 ? 1.4 : 0.0) +
+                       waves * (kper * slice * shared +
+                                0.032 * (double)std::min<int64_t>(M, nt) / s);
+      if (best_t == 0 || t < best_t) {
+        best_t = t;
+        best = {0, nt, nt <= 32 ? 4 : nt <= 64 ? 3 : nt <= 128 ? 5 : 4, s};
+      }
+    }
+  }
+  if (M > 64)
+    for (int bn : {224, 192, 128}) {
+      const int64_t tiles = ceil_div(M, 2 * BM) * ceil_div(N, bn);
+      const double slice = bn == 128 ? 0.20 : bn == 192 ? 0.225 : 0.255;
+      const double t = 3.4 + 0.0095 * bn +
+                       (double)ceil_div(tiles, std::max(1, sms / 2)) * KT * slice;
+      if (t < best_t) {
+        best_t = t;
+        best.bn = bn;
+      }
+    }
+  return best;
 }
 
 template <bool kQuant>
-static cudaError_t launch_split(const uint8_t* xq, const uint8_t* wq, LinParams p,
+static cudaError_t launch_split(const uint8_t* xq, const uint8_t* wq, LinParams p, Plan pl,
                                 cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
@@ -516,7 +554,6 @@ static cudaError_t launch_split(const uint8_t* xq, const uint8_t* wq, LinParams 
     if (err != cudaSuccess) return err;
     configured[dev] = context_id();
   }
-  Plan pl = make_plan(p.M, p.N, p.K);
   if (kQuant) pl.stages = 3;
   CUtensorMap tmW, tmX;
   if (!make_map(&tmW, wq, (uint64_t)p.K, (uint64_t)p.N, BK, WM)) return cudaErrorInvalidValue;
@@ -553,7 +590,7 @@ static cudaError_t launch_split(const uint8_t* xq, const uint8_t* wq, LinParams 
 // 14.0 at 16; K 4096 (4 slices): 6.3 / 7.3 at 8 rows, 7.4 / 7.7 at 16, 9.2 / 8.2 at 32.
 bool linear_quantizes_in_place(int64_t M, int N, int K) {
   if (M > linear::Q_ROWS) return false;
-  const linear::Plan pl = linear::make_plan(M, N, K);
+  const linear::Plan pl = linear::make_plan(M, N, K);  // (few rows: the split kernel)
   const int64_t kper = ceil_div(ceil_div(K, linear::BK), pl.nsplit);
   return kper <= linear::Q_SLICES && M * kper <= 96;
 }
@@ -580,17 +617,16 @@ cudaError_t launch_linear_fused(const uint16_t* x, const uint8_t* xq, const uint
   p.bias32 = bias32;
   p.status = device_status_ptr();
   p.wait_limit = wait_limit_cycles();
+  const Plan pl = make_plan(M, N, K);
   if (x) {
     if (!linear_quantizes_in_place(M, N, K)) return cudaErrorInvalidValue;
-    return launch_split<true>(nullptr, wq, p, stream);
+    return launch_split<true>(nullptr, wq, p, pl, stream);
   }
-  if (M > 256) {
-    int bn = 0;
-    pair_cycles(M, N, K, &bn);
-    const cudaError_t err = launch_pair(xq, wq, p, bn, stream);
-    if (err != cudaErrorNotSupported) return err;
+  if (pl.bn) {
+    const cudaError_t err = launch_pair(xq, wq, p, pl.bn, stream);
+    if (err != cudaErrorNotSupported) return err;  // the device cannot co-schedule pairs
   }
-  return launch_split<false>(xq, wq, p, stream);
+  return launch_split<false>(xq, wq, p, pl, stream);
 }
 
 }  // namespace mxmoe

@@ -175,9 +175,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
 // co-schedule pairs.
 cudaError_t launch_pair(const uint8_t* xq, const uint8_t* wq, const LinParams& p, int bn,
                         cudaStream_t stream);
-// Estimated SM cycles of the pair kernel on this product, and the tile width
-// it would take.
-double pair_cycles(int64_t M, int N, int K, int* bn);
 
 }  // namespace linear
 }  // namespace mxmoe

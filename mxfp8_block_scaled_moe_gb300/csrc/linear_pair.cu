@@ -6,15 +6,14 @@
 // tcgen05.mma (M = 256, N = BN, K = 32) issued by the even CTA reads both
 // CTAs' operands and accumulates each CTA's 128 rows in its own TMEM.
 //
-// What bounds it.  An MMA of N columns takes N / 2 tensor cycles; meanwhile each
-// SM's shared memory serves the operands (128 rows of A and N rows of B, 32
-// bytes each) and takes in what TMA writes for the next ones (128 + N / 2
-// rows): (384 + 1.5 N) * 32 B at 128 B per cycle is 160 cycles at N = 256,
-// 144 at 224, more than the tensor cycles (128, 112).  BN = 224 instead of 256
-// costs 3% of that rate and leaves 64 of the 512 TMEM columns beside two
-// accumulators: the scale factors take a ring of four k-slices there, and the
-// epilogue of a tile (bias, activation, residual, stores) runs under the next
-// tile's MMAs, which matters when K is short: a tile of K = 1152 is 36 MMAs.
+// What bounds it.  An MMA of N columns takes N / 2 tensor cycles (measured from
+// static shared memory: 448 per k-slice at BN = 224), at the power limit with the
+// clock lowered to about 1.4 GHz: 8192 x 4096 x 12288 runs at 3.0 PFLOP/s, 498 SM cycles
+// per k-slice.  BN = 224 instead of 256 leaves 64 of the 512 TMEM columns beside
+// two accumulators, enough for two scale segments, and the epilogue of a tile
+// (bias, activation, residual, stores) runs under the next tile's MMAs, which
+// matters when K is short: a tile of K = 1152 is 36 MMAs, about 4500 cycles, and
+// its epilogue as long.
 //
 // Roles (736 threads per CTA): warp 0 producer, warp 1 MMA issuer (even CTA),
 // warps 2-5 scale-factor writers, warps 6-21 epilogue (four per TMEM lane
@@ -540,23 +539,6 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                  "r"(TMEM_COLS)
                  : "memory");
   }
-}
-
-// Cycles of one MMA by tile width: the shared-memory bound above.
-static double mma_cycles(int bn) { return (384 + 1.5 * bn) * 32 / 128; }
-
-double pair_cycles(int64_t M, int N, int K, int* bn) {
-  const int64_t pairs = std::max(1, num_sms() / 2);
-  double best = 0;
-  for (int b : {224, 192, 128}) {
-    const int64_t tiles = ceil_div(M, 2 * BM) * ceil_div(N, b);
-    const double t = (double)ceil_div(tiles, pairs) * (double)ceil_div(K, BK) * 4 * mma_cycles(b);
-    if (best == 0 || t < best) {
-      best = t;
-      *bn = b;
-    }
-  }
-  return best;
 }
 
 template <int BN, bool kMX>
