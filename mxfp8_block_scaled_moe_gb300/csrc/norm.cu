@@ -11,11 +11,14 @@
 // are the bytes of mx_quantize_3d(y) and the router, which reads y, and the
 // products, which read q, see the same rows.  The sum of squares is fp32.
 //
-// One group of warps per row, 16 elements (half an MX block) per thread and
-// chunk, the row held in registers between the sum and the output: x and the
+// A group of warps per row, 16 elements (half an MX block) per thread and chunk,
+// one or two chunks per thread, all of a row's loads in flight before the first
+// is used, the row held in registers between the sum and the output: x and the
 // residual are read once, every output written once.
 //
-// Roofline: HBM-bound for many rows, latency-bound for a few.
+// Roofline: HBM-bound for many rows (16384 x 2048 with bf16 residual and bf16 rows:
+// 302 MB in 45.2 us, 6.7 TB/s, 0.98 of the measured copy rate), latency-bound for a
+// few (one row of 2048: 1.9 us in a graph).
 #include <algorithm>
 
 #include "common.cuh"
@@ -62,6 +65,23 @@ __device__ __forceinline__ void load32b(const void* p, uint32_t (&r)[8]) {
                : "memory");
 }
 
+// A thread's chunk of h: packed bf16, which is what h is without an fp32 residual,
+// or fp32.
+template <bool kF32>
+struct Chunk;
+template <>
+struct Chunk<false> {
+  uint32_t w[8];
+  __device__ __forceinline__ float get(int j) const {
+    return (j & 1) ? bf16_bits_to_float(w[j >> 1] >> 16) : bf16_bits_to_float(w[j >> 1] & 0xFFFFu);
+  }
+};
+template <>
+struct Chunk<true> {
+  float f[kChunk];
+  __device__ __forceinline__ float get(int j) const { return f[j]; }
+};
+
 // kRes: 0 no residual, 1 bf16, 2 fp32.  CPT chunks per thread.
 template <int CPT, int kRes>
 __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const Params p) {
@@ -75,48 +95,63 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const Params p)
   pdl_launch_dependents();
   pdl_wait();
 
-  float h[CPT][kChunk];
+  // every load of the row is in flight before the first is used
+  Chunk<kRes == 2> h[CPT];
+  uint32_t xw[CPT][8], rw[CPT][kRes == 1 ? 8 : 1];
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = t + i * tpr;
+    const bool in = row_ok && c < nch;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) xw[i][j] = 0;
+    if (in) load16(p.x + row * p.ldx + c * kChunk, p.x32, xw[i]);
+    if constexpr (kRes == 1) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) rw[i][j] = 0;
+      if (in) load32b(static_cast<const uint16_t*>(p.res) + row * p.H + c * kChunk, rw[i]);
+    }
+    if constexpr (kRes == 2) {
+      const float* src = static_cast<const float*>(p.res) + row * p.H + c * kChunk;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t u[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (in) load32b(src + 8 * half, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i].f[8 * half + j] = __uint_as_float(u[j]);
+      }
+    }
+  }
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int c = t + i * tpr;
     const bool in = row_ok && c < nch;
-    uint32_t xw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (in) load16(p.x + row * p.ldx + c * kChunk, p.x32, xw);
+    const int64_t at = row * p.H + c * kChunk;
+    if constexpr (kRes == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      h[i][2 * j] = bf16_bits_to_float(xw[j] & 0xFFFFu);
-      h[i][2 * j + 1] = bf16_bits_to_float(xw[j] >> 16);
-    }
-    if (in && kRes == 1) {
-      const int64_t at = row * p.H + c * kChunk;
-      uint32_t rw[8];
-      load32b(static_cast<const uint16_t*>(p.res) + at, rw);
+      for (int j = 0; j < 8; ++j) h[i].w[j] = xw[i][j];
+    } else if constexpr (kRes == 1) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        rw[j] = cvt_bf16x2(h[i][2 * j] + bf16_bits_to_float(rw[j] & 0xFFFFu),
-                           h[i][2 * j + 1] + bf16_bits_to_float(rw[j] >> 16));
-        h[i][2 * j] = bf16_bits_to_float(rw[j] & 0xFFFFu);
-        h[i][2 * j + 1] = bf16_bits_to_float(rw[j] >> 16);
+      for (int j = 0; j < 8; ++j)
+        h[i].w[j] = cvt_bf16x2(
+            bf16_bits_to_float(xw[i][j] & 0xFFFFu) + bf16_bits_to_float(rw[i][j] & 0xFFFFu),
+            bf16_bits_to_float(xw[i][j] >> 16) + bf16_bits_to_float(rw[i][j] >> 16));
+      if (in) st_v8(static_cast<uint16_t*>(p.res_out) + at, h[i].w);
+    } else {
+      uint32_t u[2][8];
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) {
+        h[i].f[j] += (j & 1) ? bf16_bits_to_float(xw[i][j >> 1] >> 16)
+                             : bf16_bits_to_float(xw[i][j >> 1] & 0xFFFFu);
+        u[j >> 3][j & 7] = __float_as_uint(h[i].f[j]);
       }
-      st_v8(static_cast<uint16_t*>(p.res_out) + at, rw);
-    }
-    if (in && kRes == 2) {
-      const int64_t at = row * p.H + c * kChunk;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t rw[8];
-        load32b(static_cast<const float*>(p.res) + at + 8 * half, rw);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          h[i][8 * half + j] += __uint_as_float(rw[j]);
-          rw[j] = __float_as_uint(h[i][8 * half + j]);
-        }
-        st_v8(static_cast<float*>(p.res_out) + at + 8 * half, rw);
+      if (in) {
+        st_v8(static_cast<float*>(p.res_out) + at, u[0]);
+        st_v8(static_cast<float*>(p.res_out) + at + 8, u[1]);
       }
     }
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+    for (int j = 0; j < kChunk; ++j) ss = fmaf(h[i].get(j), h[i].get(j), ss);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
@@ -143,8 +178,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const Params p)
           ld_nc_v8(static_cast<const float*>(p.w) + c * kChunk + 8 * half, wv);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            yw[4 * half + j] = cvt_bf16x2(h[i][8 * half + 2 * j] * r * __uint_as_float(wv[2 * j]),
-                                          h[i][8 * half + 2 * j + 1] * r *
+            yw[4 * half + j] = cvt_bf16x2(h[i].get(8 * half + 2 * j) * r * __uint_as_float(wv[2 * j]),
+                                          h[i].get(8 * half + 2 * j + 1) * r *
                                               __uint_as_float(wv[2 * j + 1]));
         }
       } else {
@@ -152,8 +187,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const Params p)
         ld_nc_v8(static_cast<const uint16_t*>(p.w) + c * kChunk, wv);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          yw[j] = cvt_bf16x2(h[i][2 * j] * r * bf16_bits_to_float(wv[j] & 0xFFFFu),
-                             h[i][2 * j + 1] * r * bf16_bits_to_float(wv[j] >> 16));
+          yw[j] = cvt_bf16x2(h[i].get(2 * j) * r * bf16_bits_to_float(wv[j] & 0xFFFFu),
+                             h[i].get(2 * j + 1) * r * bf16_bits_to_float(wv[j] >> 16));
       }
       if (p.y) st_v8(p.y + row * p.H + c * kChunk, yw);
     }
@@ -217,9 +252,19 @@ cudaError_t launch_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void*
   p.tiled = tiled;
   p.x32 = ((uintptr_t)x & 31u) == 0 && ldx % 16 == 0;
   const int nch = H / kChunk;
-  const int cpt = nch > 1024 ? 2 : 1;
+  // One CTA per row (four rows of up to 512 elements): a row's warps then wait for
+  // no other row.  Two chunks per thread for many long rows, where fewer warps
+  // meet at the barrier, and for rows of 2048 on without a residual, where one
+  // chunk's loads are too few; measured (us, bf16 residual unless said otherwise):
+  //   2048 x 12288 32.5 against 42.4 with one chunk, 4096 x 7168 34.9 / 41.7, 8192 x 4304
+  //   42.1 / 44.3; 16384 x 2048 without a residual 28.8 / 31.6, with one 37.5 / 37.8;
+  //   16384 x 1152 29.1 / 26.3 (the other way); 1 x 12288 2.9 / 2.7; with an fp32
+  //   residual 777 x 4304 9.5 / 8.4, 4096 x 7168 50.1 / 52.2.
+  const bool many = M >= 4 * (int64_t)num_sms();
+  const int longest = res32 ? 384 : res ? 256 : 127;  // chunks of a row that takes one each
+  const int cpt = nch > 1024 || (many && nch > longest) ? 2 : 1;
   p.wpr = (int)ceil_div(nch, 32 * cpt);
-  const int rows = std::max(1, 8 / p.wpr);
+  const int rows = p.wpr == 1 ? 4 : 1;
   const int64_t grid = ceil_div(M, rows);
   const dim3 block(32 * p.wpr * rows);
   const int kind = !res ? 0 : res32 ? 2 : 1;
