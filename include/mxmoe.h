@@ -395,7 +395,7 @@ mxmoe_status mxfp4_linear_mma_scales(const uint16_t* x, const uint8_t* wp, const
  *                 exactly when residual is
  *   weight        [H] bf16 or (weight_fp32 != 0) fp32
  *   y             bf16 [M, H] (NULL: not written), e.g. for the router gate
- *   q             e4m3 [M, H]
+ *   q             e4m3 [M, H], rows ldq bytes apart (ldq >= H, ldq % 16 == 0)
  *   scale         e8m0 [M, ceil(H/32)], or (mma_layout != 0) the MMA layout:
  *                 ceil(M/128) * ceil(H/128) * 512 bytes, rows past M unwritten
  * residual, residual_out, weight and y are 32-byte aligned, q and scale
@@ -405,7 +405,8 @@ mxmoe_status mxfp4_linear_mma_scales(const uint16_t* x, const uint8_t* wp, const
 mxmoe_status mx_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* residual,
                                   int residual_fp32, void* residual_out, const void* weight,
                                   int weight_fp32, float eps, int64_t M, int64_t H, uint16_t* y,
-                                  uint8_t* q, uint8_t* scale, int mma_layout, void* stream);
+                                  uint8_t* q, int64_t ldq, uint8_t* scale, int mma_layout,
+                                  void* stream);
 
 /*
  * Dense MXFP8 product with bias, activation and residual in its epilogue:
@@ -417,30 +418,32 @@ mxmoe_status mx_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* re
  *
  *   x          bf16 [M, K], MX-quantized first (the rule of mx_quantize_3d);
  *              or NULL, and then
- *   xq, xs     e4m3 [M, K] and its scales in the MMA layout (mx_add_rmsnorm_quant
+ *   xq, xs     e4m3 [M, K], rows ldxq bytes apart, and its scales in the MMA layout (mx_add_rmsnorm_quant
  *              with mma_layout, or out_q / out_s of another call)
- *   wq, ws     e4m3 [N, K] and its scales in the MMA layout
- *              (mx_scales_to_mma_layout(ws, 1, N, K))
+ *   wq, ws     e4m3 [N, K], rows ldwq bytes apart, and its scales in the MMA
+ *              layout (mx_scales_to_mma_layout(ws, 1, N, K))
  *   bias       NULL, or [N] bf16 / (bias_fp32 != 0) fp32
  *   act        0 none, 1 relu, 2 gelu (erf), 3 gelu (tanh form), 4 silu
  *   residual   NULL, or bf16 [M, N] (with out only); may be `out` itself
  *   out        bf16 [M, N], or NULL, and then
- *   out_q      e4m3 [M, N]
+ *   out_q      e4m3 [M, N], rows ldoq bytes apart
  *   out_s      its scales in the MMA layout, ceil(M/128) * ceil(N/128) * 512
  *              bytes, rows past M unwritten
  *   workspace  mxfp8_linear_fused_workspace_size(M, N, K) bytes for the current
  *              device, 256-byte aligned, when x is given (0 where few rows are
  *              quantized in the product's kernel: then it may be NULL); unused
  *              otherwise
- * All pointers 16-byte aligned.  Requires K % 16 == 0, N % 16 == 0, M < 2^24.
- * M == 0 is a no-op.
+ * All pointers 16-byte aligned, row distances multiples of 16 (of 128: the loads
+ * are faster), read only where their array is.  Requires K % 16 == 0, N % 16 == 0,
+ * M < 2^24.  M == 0 is a no-op.
  */
 size_t mxfp8_linear_fused_workspace_size(int64_t M, int64_t N, int64_t K);
-mxmoe_status mxfp8_linear_fused(const uint16_t* x, const uint8_t* xq, const uint8_t* xs,
-                                const uint8_t* wq, const uint8_t* ws, int64_t M, int64_t N,
-                                int64_t K, const void* bias, int bias_fp32, int act,
-                                const uint16_t* residual, uint16_t* out, uint8_t* out_q,
-                                uint8_t* out_s, void* workspace, size_t ws_bytes, void* stream);
+mxmoe_status mxfp8_linear_fused(const uint16_t* x, const uint8_t* xq, int64_t ldxq,
+                                const uint8_t* xs, const uint8_t* wq, int64_t ldwq,
+                                const uint8_t* ws, int64_t M, int64_t N, int64_t K,
+                                const void* bias, int bias_fp32, int act, const uint16_t* residual,
+                                uint16_t* out, uint8_t* out_q, int64_t ldoq, uint8_t* out_s,
+                                void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * The router's load-balance loss, the per-expert counts and the gradient of

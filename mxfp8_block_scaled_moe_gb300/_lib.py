@@ -79,11 +79,11 @@ _PROTOS = {
     "mx_dequantize_bf16_2d": (_I, [_P, _P, _I64, _I64, _P, _P]),
     "moe_forward_mxfp8_gated_mma_scales": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
                                                 _P, _P, _SZ, _P]),
-    "mx_add_rmsnorm_quant": (_I, [_P, _I64, _P, _I, _P, _P, _I, _F, _I64, _I64, _P, _P, _P, _I,
-                                  _P]),
+    "mx_add_rmsnorm_quant": (_I, [_P, _I64, _P, _I, _P, _P, _I, _F, _I64, _I64, _P, _P, _I64, _P,
+                                  _I, _P]),
     "mxfp8_linear_fused_workspace_size": (_SZ, [_I64, _I64, _I64]),
-    "mxfp8_linear_fused": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I, _I, _P, _P, _P, _P,
-                                _P, _SZ, _P]),
+    "mxfp8_linear_fused": (_I, [_P, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _I, _I, _P,
+                                _P, _P, _I64, _P, _P, _SZ, _P]),
     "moe_balance_loss_workspace_size": (_SZ, [_I64, _I]),
     "moe_balance_loss": (_I, [_P, _I64, _P, _P, _P, _I64, _I, _I, _F, _P, _P, _P, _P, _SZ, _P]),
 }

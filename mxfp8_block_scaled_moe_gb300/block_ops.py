@@ -4,7 +4,9 @@ output, the fused MXFP8 product and the router's load-balance loss.
 Like ``api``: argument marshalling only, every step runs in the library's
 kernels.  An MXFP8 activation is a pair ``(q, s)``: e4m3 payload uint8 [.., K]
 and its scales in the tensor-core layout, an opaque uint8 array
-[ceil(M/128) * 128, ceil(K/128) * 4].
+[ceil(M/128) * 128, ceil(K/128) * 4].  Payload rows of many are a multiple of 128
+bytes apart (``q`` is then a view of a wider array): rows that straddle cache
+lines slow the product's loads by a fifth.
 """
 
 from __future__ import annotations
@@ -13,7 +15,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .api import _need, _u8, mx_quantize_3d, mx_scales_to_mma_layout
+from .api import _u8, mx_quantize_3d, mx_scales_to_mma_layout
 
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
@@ -44,6 +46,28 @@ def _rows(t, name, dtypes):
 
 
 _HALF_OR_FLOAT = (_BF16, _F32)
+# More rows than this get payload rows a multiple of 128 bytes apart (below it
+# the product is bound by the weights' rows, and the view costs host time).
+_PAD_ROWS = 256
+
+
+def _payload(shape, M, dev):
+    """An e4m3 payload to write and the distance of its rows."""
+    K = shape[-1]
+    if M <= _PAD_ROWS or K % 128 == 0 or len(shape) != 2:
+        return _empty(shape, dtype=_U8, device=dev), K
+    ld = -(-K // 128) * 128
+    return _empty((M, ld), dtype=_U8, device=dev)[:, :K], ld
+
+
+def _payload_rows(t, name):
+    """The distance of a payload's rows: contiguous, or 2D with rows further apart."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is _U8:
+        if t.is_contiguous():
+            return t.shape[-1] if t.dim() else 0
+        if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
+            return t.stride(0)
+    _bad(t, name, (_U8,))
 
 
 def _mma_scale_shape(M: int, K: int):
@@ -92,9 +116,12 @@ def mx_add_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, bf16_out: 
         res_ptr, res_out_ptr = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    q = _empty(shape, dtype=_U8, device=dev)
-    s = _empty(_mma_scale_shape(M, H) if mma_scales else (*shape[:-1], -(-H // 32)), dtype=_U8,
-               device=dev)
+    if mma_scales:
+        q, ldq = _payload(shape, M, dev)
+        s = _empty(_mma_scale_shape(M, H), dtype=_U8, device=dev)
+    else:
+        q, ldq = _empty(shape, dtype=_U8, device=dev), H
+        s = _empty((*shape[:-1], -(-H // 32)), dtype=_U8, device=dev)
     out = {"q": q, "s": s}
     if residual is not None:
         out["residual"] = residual_out
@@ -103,7 +130,7 @@ def mx_add_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, bf16_out: 
         y_ptr = y.data_ptr()
     rc = _lib.load().mx_add_rmsnorm_quant(
         x.data_ptr(), ldx, res_ptr, res32, res_out_ptr, weight.data_ptr(), weight.dtype is _F32,
-        eps, M, H, y_ptr, q.data_ptr(), s.data_ptr(), mma_scales, _raw_stream(dev.index))
+        eps, M, H, y_ptr, q.data_ptr(), ldq, s.data_ptr(), mma_scales, _raw_stream(dev.index))
     if rc:
         _lib.check("mx_add_rmsnorm_quant", rc)
     return out
@@ -118,17 +145,19 @@ def mxfp8_linear_fused(x, wq, ws_mma, bias=None, act=None, residual=None, mx_out
     """act(x . wq^T + bias) + residual with an MXFP8 product.
 
     x: bf16 [.., K] (MX-quantized per token on the device) or an MXFP8 pair
-    (q, s) with tensor-core scales; wq e4m3 [N, K], ws_mma its scales in the
-    tensor-core layout; bias bf16 or fp32 [N]; act one of "none", "relu",
+    (q, s) with tensor-core scales; wq e4m3 [N, K] (its rows may be further
+    apart), ws_mma its scales in the tensor-core layout; bias bf16 or fp32 [N]; act one of "none", "relu",
     "gelu", "gelu_tanh", "silu"; residual bf16 [.., N].  Returns bf16 [.., N],
     or with ``mx_out`` the MXFP8 pair of act(..) (no residual)."""
     wq = _u8(wq)
-    _need(wq, "wq", _U8, 2)
     _check_weight(wq, ws_mma, bias, act)
     return _fused(x, wq, ws_mma, bias, ACTIVATIONS[act], residual, mx_out, out, workspace)
 
 
 def _check_weight(wq, ws_mma, bias, act):
+    _payload_rows(wq, "wq")
+    if wq.dim() != 2:
+        raise ValueError(f"wq: expected 2 dims, got {tuple(wq.shape)}")
     N, K = wq.shape
     _rows(ws_mma, "ws_mma", (_U8,))
     rows, cols = _mma_scale_shape(N, K)
@@ -147,12 +176,12 @@ def _fused(x, wq, ws_mma, bias, act, residual, mx_out, out, workspace):
     function of (M, device) that gives one (or None) for bf16 input."""
     N, K = wq.shape
     x_ptr = xq_ptr = xs_ptr = ws_ptr = res_ptr = out_ptr = oq_ptr = os_ptr = None
-    ws_bytes = 0
+    ws_bytes = ldx = ldo = 0
     lib = _lib.load()
     if type(x) is tuple:
         xin, xs = x
         xin = _u8(xin)
-        _rows(xin, "x[0]", (_U8,))
+        ldx = _payload_rows(xin, "x[0]")
         _rows(xs, "x[1]", (_U8,))
     else:
         xin, xs = x, None
@@ -187,8 +216,8 @@ def _fused(x, wq, ws_mma, bias, act, residual, mx_out, out, workspace):
     if mx_out:
         if out is not None:
             raise ValueError("out holds a bf16 result")
-        out = (_empty(shape, dtype=_U8, device=dev),
-               _empty(_mma_scale_shape(M, N), dtype=_U8, device=dev))
+        oq, ldo = _payload(shape, M, dev)
+        out = (oq, _empty(_mma_scale_shape(M, N), dtype=_U8, device=dev))
         oq_ptr, os_ptr = out[0].data_ptr(), out[1].data_ptr()
     else:
         if out is None:
@@ -200,8 +229,9 @@ def _fused(x, wq, ws_mma, bias, act, residual, mx_out, out, workspace):
         out_ptr = out.data_ptr()
     bias_ptr, bias32 = (None, 0) if bias is None else (bias.data_ptr(), bias.dtype is _F32)
     rc = lib.mxfp8_linear_fused(
-        x_ptr, xq_ptr, xs_ptr, wq.data_ptr(), ws_mma.data_ptr(), M, N, K, bias_ptr, bias32, act,
-        res_ptr, out_ptr, oq_ptr, os_ptr, ws_ptr, ws_bytes, _raw_stream(dev.index))
+        x_ptr, xq_ptr, ldx, xs_ptr, wq.data_ptr(), wq.stride(0), ws_mma.data_ptr(), M, N, K,
+        bias_ptr, bias32, act, res_ptr, out_ptr, oq_ptr, ldo, os_ptr, ws_ptr, ws_bytes,
+        _raw_stream(dev.index))
     if rc:
         _lib.check("mxfp8_linear_fused", rc)
     return out
@@ -212,15 +242,18 @@ class MXFP8FusedLinear:
 
     Weights as ``MXFP8Linear``: ``from_bf16`` quantizes at load, the
     constructor takes an offline checkpoint's payload and [N, ceil(K/32)]
-    scales, which are re-laid once.  Calls take bf16 rows or an MXFP8 pair."""
+    scales, which are re-laid once (a payload of K % 128 != 0 as well, its rows
+    to a multiple of 128 bytes apart).  Calls take bf16 rows or an MXFP8 pair."""
 
     def __init__(self, wq, ws, bias=None, act=None):
         self.wq = _u8(wq)
         self.N, self.K = self.wq.shape
         self.ws_mma = mx_scales_to_mma_layout(ws, self.K)
         self.bias, self.act = bias, act
-        _need(self.wq, "wq", _U8, 2)
         _check_weight(self.wq, self.ws_mma, bias, act)
+        if self.K % 128:
+            wide = _empty((self.N, -(-self.K // 128) * 128), dtype=_U8, device=self.wq.device)
+            self.wq = wide[:, :self.K].copy_(self.wq)
         self._ws = None
         self._need = {}  # rows -> workspace bytes
 

@@ -682,8 +682,9 @@ static inline bool aligned(const void* p, unsigned bytes) {
 mxmoe_status mx_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* residual,
                                   int residual_fp32, void* residual_out, const void* weight,
                                   int weight_fp32, float eps, int64_t M, int64_t H, uint16_t* y,
-                                  uint8_t* q, uint8_t* scale, int mma_layout, void* stream) {
-  if (M < 0 || M >= (1ll << 31) || H <= 0 || H % 16 != 0 || ldx < H || !(eps >= 0.f))
+                                  uint8_t* q, int64_t ldq, uint8_t* scale, int mma_layout,
+                                  void* stream) {
+  if (M < 0 || M >= (1ll << 31) || H <= 0 || H % 16 != 0 || ldx < H || ldq < H || !(eps >= 0.f))
     return MXMOE_ERR_SHAPE;
   if (H > 32768) return MXMOE_ERR_UNSUPPORTED;
   if (M == 0) return MXMOE_OK;
@@ -692,16 +693,21 @@ mxmoe_status mx_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* re
   MXMOE_CHECK_PTR(q);
   MXMOE_CHECK_PTR(scale);
   if ((residual == nullptr) != (residual_out == nullptr)) return MXMOE_ERR_NULL;
-  if (ldx % 8 != 0 || !aligned(weight, 32) || !aligned(residual, 32) ||
+  if (ldx % 8 != 0 || ldq % 16 != 0 || !aligned(weight, 32) || !aligned(residual, 32) ||
       !aligned(residual_out, 32) || !aligned(y, 32))
     return MXMOE_ERR_ALIGN;
   return from_cuda(launch_add_rmsnorm_quant(x, ldx, residual, residual_fp32 != 0, residual_out,
-                                            weight, weight_fp32 != 0, eps, M, (int)H, y, q, scale,
+                                            weight, weight_fp32 != 0, eps, M, (int)H, y, q, ldq, scale,
                                             mma_layout != 0, (cudaStream_t)stream));
 }
 
-// Workspace of mxfp8_linear_fused with bf16 input: xq [M, K] | xs in the MMA layout.
-static size_t fused_xs_offset(int64_t M, int64_t K) { return align256((size_t)M * K); }
+// Workspace of mxfp8_linear_fused with bf16 input: xq, rows a multiple of 128 bytes
+// apart (rows that straddle cache lines cost the loads: 16384 x 1152 x 4304 79 us
+// with rows 4304 bytes apart, 63 at 4352) | xs in the MMA layout.
+static int64_t fused_row(int64_t K) { return (K + 127) / 128 * 128; }
+static size_t fused_xs_offset(int64_t M, int64_t K) {
+  return align256((size_t)M * (size_t)fused_row(K));
+}
 
 size_t mxfp8_linear_fused_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (!linear_shape_ok(M, N, K) || M >= (1ll << 24) || M == 0 ||
@@ -711,17 +717,20 @@ size_t mxfp8_linear_fused_workspace_size(int64_t M, int64_t N, int64_t K) {
          align256((size_t)((M + 127) / 128) * (size_t)((K + 127) / 128) * 512);
 }
 
-mxmoe_status mxfp8_linear_fused(const uint16_t* x, const uint8_t* xq, const uint8_t* xs,
-                                const uint8_t* wq, const uint8_t* ws, int64_t M, int64_t N,
-                                int64_t K, const void* bias, int bias_fp32, int act,
-                                const uint16_t* residual, uint16_t* out, uint8_t* out_q,
-                                uint8_t* out_s, void* workspace, size_t ws_bytes, void* stream) {
+mxmoe_status mxfp8_linear_fused(const uint16_t* x, const uint8_t* xq, int64_t ldxq,
+                                const uint8_t* xs, const uint8_t* wq, int64_t ldwq,
+                                const uint8_t* ws, int64_t M, int64_t N, int64_t K,
+                                const void* bias, int bias_fp32, int act, const uint16_t* residual,
+                                uint16_t* out, uint8_t* out_q, int64_t ldoq, uint8_t* out_s,
+                                void* workspace, size_t ws_bytes, void* stream) {
   if (!linear_shape_ok(M, N, K) || M >= (1ll << 24) || act < 0 || act >= ACT_COUNT)
     return MXMOE_ERR_SHAPE;
   // one output form; the residual joins a bf16 result only
   if (out && (out_q || out_s)) return MXMOE_ERR_UNSUPPORTED;
-  if (residual && !out) return MXMOE_ERR_UNSUPPORTED;
   if (M == 0) return MXMOE_OK;
+  if (residual && !out) return MXMOE_ERR_UNSUPPORTED;
+  if (ldwq < K || (!x && ldxq < K) || (!out && ldoq < N)) return MXMOE_ERR_SHAPE;
+  if (ldwq % 16 != 0 || (!x && ldxq % 16 != 0) || (!out && ldoq % 16 != 0)) return MXMOE_ERR_ALIGN;
   MXMOE_CHECK_PTR(wq);
   MXMOE_CHECK_PTR(ws);
   if (bias) MXMOE_CHECK_PTR(bias);
@@ -741,10 +750,11 @@ mxmoe_status mxfp8_linear_fused(const uint16_t* x, const uint8_t* xq, const uint
         return MXMOE_ERR_WORKSPACE;
       if (!aligned(workspace, 256)) return MXMOE_ERR_ALIGN;
       uint8_t* base = (uint8_t*)workspace;
-      if (launch_mx_quantize_tiled(x, M, K, base, base + fused_xs_offset(M, K), nullptr, st) !=
-          cudaSuccess)
+      if (launch_mx_quantize_tiled(x, M, K, base, base + fused_xs_offset(M, K), nullptr, st, false,
+                                   fused_row(K)) != cudaSuccess)
         return MXMOE_ERR_CUDA;
       xq = base;
+      ldxq = fused_row(K);
       xs = base + fused_xs_offset(M, K);
       x = nullptr;
     }
@@ -752,8 +762,8 @@ mxmoe_status mxfp8_linear_fused(const uint16_t* x, const uint8_t* xq, const uint
     MXMOE_CHECK_PTR(xq);
     MXMOE_CHECK_PTR(xs);
   }
-  return from_cuda(launch_linear_fused(x, xq, xs, wq, ws, M, (int)N, (int)K, bias, bias_fp32 != 0,
-                                       act, residual, out, out_q, out_s, st));
+  return from_cuda(launch_linear_fused(x, xq, ldxq, xs, wq, ldwq, ws, M, (int)N, (int)K, bias,
+                                       bias_fp32 != 0, act, residual, out, out_q, ldoq, out_s, st));
 }
 
 size_t moe_balance_loss_workspace_size(int64_t T, int E) {

@@ -27,10 +27,11 @@ cudaError_t launch_mx_quantize(const uint16_t* x, int64_t rows, int64_t K, uint8
                                uint8_t* scale, cudaStream_t stream);
 // Any K % 16 == 0 (ceil(K/32) scales, a partial last block of 16), scales
 // written in the tiled layout (KT = ceil(K/128)); offsets (nullable) <- {0, rows}.
-// fp4: MXFP4 rows, q [rows, K/2] packed e2m1, K % 32 == 0.
+// fp4: MXFP4 rows, q [rows, K/2] packed e2m1, K % 32 == 0.  ldq: MXFP8 payload
+// rows apart, in bytes (0: K).
 cudaError_t launch_mx_quantize_tiled(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q,
                                      uint8_t* scale_tiled, int64_t* offsets, cudaStream_t stream,
-                                     bool fp4 = false);
+                                     bool fp4 = false, int64_t ldq = 0);
 // MXFP4 (packed e2m1, W4A8 weights): q [rows, K/2], scale [rows, K/32].
 cudaError_t launch_mx_quantize_fp4(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q,
                                    uint8_t* scale, cudaStream_t stream);
@@ -129,21 +130,23 @@ cudaError_t launch_gemm_chain(const uint8_t* xq, const uint8_t* xs, const uint8_
 int gemm_bf16_ksplit(int64_t M, int N, int K, bool packed_fp4 = false);
 
 // Residual addition + RMS norm + MXFP8 rows (norm.cu).  res (nullable) bf16,
-// fp32 with res32; w fp32 with w32; y nullable; ldx in elements.
+// fp32 with res32; w fp32 with w32; y nullable; ldx, ldq in elements.
 cudaError_t launch_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* res, bool res32,
                                      void* res_out, const void* w, bool w32, float eps, int64_t M,
-                                     int H, uint16_t* y, uint8_t* q, uint8_t* s, bool tiled,
-                                     cudaStream_t stream);
+                                     int H, uint16_t* y, uint8_t* q, int64_t ldq, uint8_t* s,
+                                     bool tiled, cudaStream_t stream);
 
 // MXFP8 product with bias, activation and residual (linear.cu).  Either x (bf16,
 // only where linear_quantizes_in_place) or xq / xs; scales in the MMA layout;
-// bias, residual nullable; either out (bf16) or oq / os (MXFP8).
+// ldx, ldw, ldo: payload rows apart, in bytes; bias, residual nullable; either
+// out (bf16) or oq / os (MXFP8).
 bool linear_quantizes_in_place(int64_t M, int N, int K);
 enum : int { ACT_NONE = 0, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU, ACT_COUNT };
-cudaError_t launch_linear_fused(const uint16_t* x, const uint8_t* xq, const uint8_t* xs,
-                                const uint8_t* wq, const uint8_t* ws, int64_t M, int N, int K,
-                                const void* bias, bool bias32, int act, const uint16_t* residual,
-                                uint16_t* out, uint8_t* oq, uint8_t* os, cudaStream_t stream);
+cudaError_t launch_linear_fused(const uint16_t* x, const uint8_t* xq, int64_t ldx,
+                                const uint8_t* xs, const uint8_t* wq, int64_t ldw,
+                                const uint8_t* ws, int64_t M, int N, int K, const void* bias,
+                                bool bias32, int act, const uint16_t* residual, uint16_t* out,
+                                uint8_t* oq, int64_t ldo, uint8_t* os, cudaStream_t stream);
 
 // Load-balance loss, counts and the logits' gradient (balance.cu).  mask,
 // counts_in, dlogits nullable.

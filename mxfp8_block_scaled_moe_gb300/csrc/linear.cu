@@ -119,7 +119,7 @@ __device__ __forceinline__ void finish_token(const LinParams& p, int64_t t, int 
   const uint32_t sb = e8m0_from_amax_bits(m);
   const float inv = inv_scale_from_e8m0(sb);
   if (in)
-    *reinterpret_cast<uint32_t*>(p.oq + t * p.N + n) =
+    *reinterpret_cast<uint32_t*>(p.oq + t * p.ldo + n) =
         cvt_e4m3x4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
   // the 128 columns' four scale bytes are one word of the MMA layout; slots
   // past the row's last block hold 127
@@ -556,9 +556,9 @@ static cudaError_t launch_split(const uint8_t* xq, const uint8_t* wq, LinParams 
   }
   if (kQuant) pl.stages = 3;
   CUtensorMap tmW, tmX;
-  if (!make_map(&tmW, wq, (uint64_t)p.K, (uint64_t)p.N, BK, WM)) return cudaErrorInvalidValue;
+  if (!make_map_ld(&tmW, wq, p.K, p.N, p.ldw, WM)) return cudaErrorInvalidValue;
   if (kQuant) tmX = tmW;  // not read
-  else if (!make_map(&tmX, xq, (uint64_t)p.K, (uint64_t)p.M, BK, (uint32_t)pl.NT))
+  else if (!make_map_ld(&tmX, xq, p.K, p.M, p.ldx, (uint32_t)pl.NT))
     return cudaErrorInvalidValue;
   p.NT = pl.NT;
   p.stages = pl.stages;
@@ -595,10 +595,11 @@ bool linear_quantizes_in_place(int64_t M, int N, int K) {
   return kper <= linear::Q_SLICES && M * kper <= 96;
 }
 
-cudaError_t launch_linear_fused(const uint16_t* x, const uint8_t* xq, const uint8_t* xs,
-                                const uint8_t* wq, const uint8_t* ws, int64_t M, int N, int K,
-                                const void* bias, bool bias32, int act, const uint16_t* residual,
-                                uint16_t* out, uint8_t* oq, uint8_t* os, cudaStream_t stream) {
+cudaError_t launch_linear_fused(const uint16_t* x, const uint8_t* xq, int64_t ldx,
+                                const uint8_t* xs, const uint8_t* wq, int64_t ldw,
+                                const uint8_t* ws, int64_t M, int N, int K, const void* bias,
+                                bool bias32, int act, const uint16_t* residual, uint16_t* out,
+                                uint8_t* oq, int64_t ldo, uint8_t* os, cudaStream_t stream) {
   using namespace linear;
   if (M == 0) return cudaSuccess;
   LinParams p = {};
@@ -609,6 +610,9 @@ cudaError_t launch_linear_fused(const uint16_t* x, const uint8_t* xq, const uint
   p.res = residual;
   p.out = out;
   p.oq = oq;
+  p.ldo = ldo;
+  p.ldx = ldx;
+  p.ldw = ldw;
   p.os = os;
   p.M = M;
   p.N = N;

@@ -16,14 +16,15 @@ struct LinParams {
   const void* bias;        // [N] or null
   const uint16_t* res;     // [M, N] bf16 or null
   uint16_t* out;           // [M, N] bf16 (bf16 output)
-  uint8_t* oq;             // [M, N] e4m3 (MXFP8 output)
+  uint8_t* oq;             // [M, N] e4m3 (MXFP8 output), rows ldo bytes apart
+  int64_t ldo, ldx, ldw;   // payload rows apart: output, activations, weights
   uint8_t* os;             // MMA layout, KT_out = ceil(N/128)
   int64_t M;
   int N, K, act;
   bool bias32;
   int NT, stages, nsplit;  // split kernel: token tile, pipeline stages, K ranges
   int tiles_n, tiles;      // pair kernel: n-tiles, tiles
-  bool v32;                // pair kernel: out / residual rows are 32-byte aligned
+  bool v32;                // pair kernel: rows of out and residual, or of oq, are 32-byte aligned
   int* status;
   long long wait_limit;
 };
@@ -169,6 +170,20 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
+}
+
+// e4m3 [outer, inner], rows ld bytes apart (a multiple of 16), 128-byte swizzled box.
+inline bool make_map_ld(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                        uint64_t ld, uint32_t box_outer) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {ld};
+  cuuint32_t box[2] = {(cuuint32_t)BK, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // CTA pairs (linear_pair.cu).  cudaErrorNotSupported: the device cannot

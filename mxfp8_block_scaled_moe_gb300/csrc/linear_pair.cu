@@ -144,9 +144,13 @@ __device__ __forceinline__ void finish_mx(const LinParams& p, int64_t row, bool 
     o[i] = cvt_e4m3x4(x, y, z, w);
   }
   if (!valid) return;
-  uint8_t* dst = p.oq + row * p.N + n;
-  st_v4(dst, make_uint4(o[0], o[1], o[2], o[3]));
-  if (hi) st_v4(dst + 16, make_uint4(o[4], o[5], o[6], o[7]));
+  uint8_t* dst = p.oq + row * p.ldo + n;
+  if (p.v32 && hi) {
+    st_v8(dst, o);
+  } else {
+    st_v4(dst, make_uint4(o[0], o[1], o[2], o[3]));
+    if (hi) st_v4(dst + 16, make_uint4(o[4], o[5], o[6], o[7]));
+  }
   const int KT = (p.N + 127) / 128, j = n >> 5;
   p.os[tiled_scale_offset(row, j, KT)] = (uint8_t)sb;
   if (n + 32 >= p.N)  // the row's last block: the slots after it hold 127
@@ -583,10 +587,11 @@ static cudaError_t launch_pair_bn(const uint8_t* xq, const uint8_t* wq, LinParam
   const int64_t tiles = ceil_div(p.M, 2 * BM) * p.tiles_n;
   if (tiles >= (1ll << 31)) return cudaErrorNotSupported;
   p.tiles = (int)tiles;
-  p.v32 = (((uintptr_t)p.out | (uintptr_t)p.res) & 31u) == 0;
+  p.v32 = kMX ? (((uintptr_t)p.oq | (uintptr_t)p.ldo) & 31u) == 0
+              : (((uintptr_t)p.out | (uintptr_t)p.res) & 31u) == 0;
   CUtensorMap tmX, tmW;
-  if (!make_map(&tmX, xq, (uint64_t)p.K, (uint64_t)p.M, BK, BM) ||
-      !make_map(&tmW, wq, (uint64_t)p.K, (uint64_t)p.N, BK, BN / 2))
+  if (!make_map_ld(&tmX, xq, p.K, p.M, p.ldx, BM) ||
+      !make_map_ld(&tmW, wq, p.K, p.N, p.ldw, BN / 2))
     return cudaErrorInvalidValue;
   const int clusters = (int)std::min<int64_t>(
       {tiles, (int64_t)max_clusters[dev], (int64_t)std::max(1, num_sms() / 2)});

@@ -41,6 +41,7 @@ struct Params {
   int H, wpr;  // row length, warps per row
   uint16_t* y;
   uint8_t* q;
+  int64_t ldq;
   uint8_t* s;
   bool w32, tiled, x32;  // fp32 weight, tiled scales, 32-byte aligned x rows
 };
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const Params p)
                           bf16_bits_to_float(yw[2 * j] >> 16) * inv,
                           bf16_bits_to_float(yw[2 * j + 1] & 0xFFFFu) * inv,
                           bf16_bits_to_float(yw[2 * j + 1] >> 16) * inv);
-      st_v4(p.q + row * p.H + c * kChunk, make_uint4(o[0], o[1], o[2], o[3]));
+      st_v4(p.q + row * p.ldq + c * kChunk, make_uint4(o[0], o[1], o[2], o[3]));
     }
     // four blocks' scale bytes (eight lanes) go out as one word; a slot past
     // the row's last block holds 127 (scale 1) in the tiled layout
@@ -232,8 +233,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const Params p)
 
 cudaError_t launch_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* res, bool res32,
                                      void* res_out, const void* w, bool w32, float eps, int64_t M,
-                                     int H, uint16_t* y, uint8_t* q, uint8_t* s, bool tiled,
-                                     cudaStream_t stream) {
+                                     int H, uint16_t* y, uint8_t* q, int64_t ldq, uint8_t* s,
+                                     bool tiled, cudaStream_t stream) {
   using namespace norm;
   if (M == 0) return cudaSuccess;
   Params p;
@@ -247,6 +248,7 @@ cudaError_t launch_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void*
   p.H = H;
   p.y = y;
   p.q = q;
+  p.ldq = ldq;
   p.s = s;
   p.w32 = w32;
   p.tiled = tiled;

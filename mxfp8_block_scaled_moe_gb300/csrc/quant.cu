@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const uint16_t* __rest
 template <bool kV8, bool kTiled, bool kFp4 = false>
 __global__ void __launch_bounds__(256) mx_quantize_rows_kernel(const uint16_t* __restrict__ x,
                                                                int64_t rows, int64_t K,
-                                                               uint8_t* __restrict__ q,
+                                                               uint8_t* __restrict__ q, int64_t ldq,
                                                                uint8_t* __restrict__ scale,
                                                                int64_t* __restrict__ offsets) {
   pdl_launch_dependents();
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(256) mx_quantize_rows_kernel(const uint16_t* _
     const int64_t r = b / nbr;
     const int j = (int)(b - r * nbr);
     const uint16_t* xb = x + r * K + 32 * j;
-    uint8_t* qb = q + r * K + 32 * j;
+    uint8_t* qb = q + r * ldq + 32 * j;
     uint32_t sb;
     if (kFp4) {
       uint32_t w[16], o[4];
@@ -108,7 +108,8 @@ __global__ void __launch_bounds__(256) mx_quantize_rows_kernel(const uint16_t* _
 
 template <bool kTiled, bool kFp4 = false>
 static cudaError_t launch_rows(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q,
-                               uint8_t* scale, cudaStream_t stream, int64_t* offsets = nullptr) {
+                               uint8_t* scale, cudaStream_t stream, int64_t* offsets = nullptr,
+                               int64_t ldq = 0) {
   const int64_t n = rows * ((K + 31) / 32);
   if (n == 0) return cudaSuccess;
   int64_t blocks = ceil_div(n, 256);
@@ -116,18 +117,18 @@ static cudaError_t launch_rows(const uint16_t* x, int64_t rows, int64_t K, uint8
   if (blocks > cap) blocks = cap;
   auto kern = ((uintptr_t)x & 31u) == 0 ? mx_quantize_rows_kernel<true, kTiled, kFp4>
                                         : mx_quantize_rows_kernel<false, kTiled, kFp4>;
-  return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, stream, x, rows, K, q, scale,
-                    offsets);
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, stream, x, rows, K, q,
+                    ldq ? ldq : K, scale, offsets);
 }
 
 cudaError_t launch_mx_quantize_tiled(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q,
                                      uint8_t* scale_tiled, int64_t* offsets, cudaStream_t stream,
-                                     bool fp4) {
+                                     bool fp4, int64_t ldq) {
   if (fp4) {
     if (K % 32 != 0) return cudaErrorInvalidValue;
     return launch_rows<true, true>(x, rows, K, q, scale_tiled, stream, offsets);
   }
-  return launch_rows<true>(x, rows, K, q, scale_tiled, stream, offsets);
+  return launch_rows<true>(x, rows, K, q, scale_tiled, stream, offsets, ldq);
 }
 
 cudaError_t launch_mx_quantize(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q,

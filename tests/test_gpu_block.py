@@ -283,6 +283,32 @@ def test_linear_in_place_strided_and_repeated(mm):
     assert torch.equal(other, want)
 
 
+def test_linear_payload_rows_further_apart(mm):
+    """Pairs and weights whose rows are 16 bytes or more apart from packed ones."""
+    for M in (7, 300):
+        for N, K in ((400, 336), (272, 512)):
+            x = randn(M, M, K).bfloat16()
+            lin = mm.MXFP8FusedLinear.from_bf16(randn(2, N, K, scale=0.02).bfloat16(), act="silu")
+            r = mm.mx_add_rmsnorm_quant(x, torch.ones(K, device=DEV), mma_scales=True)
+            q, want = r["q"].contiguous(), lin((r["q"], r["s"]))
+            mid = lin((r["q"], r["s"]), mx_out=True)
+            assert torch.equal(lin((q, r["s"])), want)
+            for pad in (16, 48, 128):
+                wide = torch.full((M, K + pad), 0x7F, dtype=torch.uint8, device=DEV)
+                wide[:, :K] = q
+                w = torch.full((N, K + pad), 0x7F, dtype=torch.uint8, device=DEV)
+                w[:, :K] = lin.wq
+                got = mm.mxfp8_linear_fused((wide[:, :K], r["s"]), w[:, :K], lin.ws_mma, act="silu")
+                assert torch.equal(got, want)
+                m = mm.mxfp8_linear_fused((wide[:, :K], r["s"]), w[:, :K], lin.ws_mma, act="silu",
+                                          mx_out=True)
+                assert torch.equal(m[0], mid[0])
+                assert np.array_equal(untile(m[1], M, N)[0], untile(mid[1], M, N)[0])
+            with pytest.raises(mm.api._lib.MXMoEError):
+                mm.mxfp8_linear_fused((torch.empty(M, K + 8, dtype=torch.uint8, device=DEV)[:, :K],
+                                       r["s"]), lin.wq, lin.ws_mma)
+
+
 def test_linear_rows_do_not_depend_on_their_neighbours(mm):
     """A row of NaN, of infinities and of zeros beside ordinary ones."""
     lin = mm.MXFP8FusedLinear.from_bf16(randn(2, 256, 512, scale=0.02).bfloat16())

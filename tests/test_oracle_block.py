@@ -87,14 +87,15 @@ P16 = C.c_void_p(4096 + 16)
 
 def _norm(lib, **kw):
     a = dict(x=P, ldx=64, residual=P, residual_fp32=0, residual_out=P, weight=P, weight_fp32=0,
-             eps=1e-6, M=4, H=64, y=P, q=P, scale=P, mma=0, stream=NUL)
+             eps=1e-6, M=4, H=64, y=P, q=P, ldq=64, scale=P, mma=0, stream=NUL)
     a.update(kw)
     return lib.mx_add_rmsnorm_quant(*a.values())
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(H=72), 3), (dict(H=0), 3), (dict(M=-1), 3), (dict(ldx=48), 3), (dict(M=1 << 31), 3),
-    (dict(eps=-1.0), 3), (dict(eps=float("nan")), 3), (dict(H=32784, ldx=32784), 4),
+    (dict(eps=-1.0), 3), (dict(eps=float("nan")), 3), (dict(H=32784, ldx=32784, ldq=32784), 4),
+    (dict(ldq=48), 3), (dict(ldq=72), 2),
     (dict(x=NUL), 1), (dict(weight=NUL), 1), (dict(q=NUL), 1), (dict(scale=NUL), 1),
     (dict(residual=NUL), 1), (dict(residual_out=NUL), 1), (dict(x=ODD), 2), (dict(ldx=68), 2),
     (dict(weight=P16), 2), (dict(residual=P16), 2), (dict(residual_out=P16), 2), (dict(y=P16), 2),
@@ -104,8 +105,8 @@ def test_norm_refusals(lib, kw, code):
 
 
 def _linear(lib, **kw):
-    a = dict(x=P, xq=NUL, xs=NUL, wq=P, ws=P, M=4, N=64, K=64, bias=P, bias32=0, act=1, residual=P,
-             out=P, oq=NUL, os=NUL, ws_=P, ws_bytes=1 << 30, stream=NUL)
+    a = dict(x=P, xq=NUL, ldx=64, xs=NUL, wq=P, ldw=64, ws=P, M=4, N=64, K=64, bias=P, bias32=0,
+             act=1, residual=P, out=P, oq=NUL, ldo=64, os=NUL, ws_=P, ws_bytes=1 << 30, stream=NUL)
     a.update(kw)
     return lib.mxfp8_linear_fused(*a.values())
 
@@ -117,7 +118,10 @@ def _linear(lib, **kw):
     (dict(x=NUL, xq=P), 1), (dict(out=NUL, residual=NUL), 1),
     (dict(out=NUL, residual=NUL, oq=P), 1), (dict(x=ODD), 2), (dict(wq=ODD), 2),
     (dict(bias=ODD), 2), (dict(residual=ODD), 2), (dict(out=ODD), 2), (dict(M=33, ws_=NUL), 5),
-    (dict(M=33, ws_bytes=256), 5), (dict(M=33, ws_=P16), 2), (dict(M=0, x=NUL, wq=NUL, ws_=NUL), 0)])
+    (dict(ldw=48), 3), (dict(ldw=72), 2),
+    (dict(x=NUL, xq=P, xs=P, ldx=48), 3), (dict(x=NUL, xq=P, xs=P, ldx=72), 2),
+    (dict(out=NUL, residual=NUL, oq=P, os=P, ldo=48), 3),
+    (dict(out=NUL, residual=NUL, oq=P, os=P, ldo=72), 2), (dict(M=33, ws_bytes=256), 5), (dict(M=33, ws_=P16), 2), (dict(M=0, x=NUL, wq=NUL, ws_=NUL), 0)])
 def test_linear_refusals(lib, kw, code):
     assert _linear(lib, **kw) == code
 
