@@ -109,6 +109,26 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     return lib
 
 
+_binding = None
+
+
+def load_binding():
+    """Load (once) and return the native half of ``block_ops``, bound to the library."""
+    global _binding
+    if _binding is None:
+        lib = load()
+        path = os.path.join(_PKG, "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"_binding.so not found at {path}: build it first "
+                               "(python -m mxfp8_block_scaled_moe_gb300.build)")
+        from . import _binding as native
+        native.bind(*(C.cast(getattr(lib, n), C.c_void_p).value for n in (
+            "mx_add_rmsnorm_quant", "mxfp8_linear_fused", "mxfp8_linear_fused_workspace_size",
+            "moe_balance_loss", "moe_balance_loss_workspace_size")))
+        _binding = native
+    return _binding
+
+
 class MXMoEError(RuntimeError):
     def __init__(self, fn: str, code: int):
         msg = load().mxmoe_status_string(code).decode()

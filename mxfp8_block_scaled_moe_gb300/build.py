@@ -2,16 +2,20 @@
 
 Each CUDA translation unit is compiled in parallel, then linked into
 ``mxfp8_block_scaled_moe_gb300/libmxmoe.so`` with a static CUDA runtime, so
-the library needs nothing but the NVIDIA driver at run time.  Object files go
-to ``_build/`` at the repository root.  No CMake.
+the library needs nothing but the NVIDIA driver at run time.  Beside it, g++
+compiles ``csrc/binding.cpp`` against the installed PyTorch's headers into the
+native half of ``block_ops``, ``_binding.so``.  Object files go to ``_build/`` at
+the repository root.  No CMake.
 """
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -19,6 +23,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libmxmoe.so")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 
 SOURCES = ["api.cu", "quant.cu", "route.cu", "finalize.cu", "gemm.cu", "gemm2sm.cu", "noalloc.cu",
            "router.cu", "norm.cu", "linear.cu", "linear_pair.cu", "balance.cu"]
@@ -34,6 +39,16 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libmxmoe.so")
 
 
+def _binding_command(out: str) -> list:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            "-I" + INCLUDE, "-I" + os.path.join(torch, "include"),
+            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
+            "-o", out, os.path.join(CSRC, "binding.cpp"), "-L" + os.path.join(torch, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+
+
 def _deps_mtime() -> float:
     paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + \
         [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [os.path.abspath(__file__)]
@@ -42,7 +57,8 @@ def _deps_mtime() -> float:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if stale) and return the path of libmxmoe.so."""
-    if not force and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= _deps_mtime():
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _deps_mtime()
+                         for p in (LIB_PATH, BINDING_PATH)):
         return LIB_PATH
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -50,10 +66,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
     objs = []
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
-        log = open(os.path.join(BUILD_DIR, src.replace(".cu", ".log")), "w")
+        log = open(os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".log"), "w")
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
         procs.append((src, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT), log))
         objs.append(obj)
+    log = open(os.path.join(BUILD_DIR, "binding.log"), "w")
+    binding_tmp = BINDING_PATH + ".tmp"
+    procs.append(("binding.cpp", subprocess.Popen(_binding_command(binding_tmp), stdout=log,
+                                                 stderr=subprocess.STDOUT), log))
     failed = []
     for src, p, log in procs:
         rc = p.wait()
@@ -63,18 +83,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if failed:
         msgs = []
         for src in failed:
-            with open(os.path.join(BUILD_DIR, src.replace(".cu", ".log"))) as f:
+            with open(os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".log")) as f:
                 msgs.append(f"--- {src}\n" + f.read()[-4000:])
-        raise RuntimeError("nvcc failed:\n" + "\n".join(msgs))
+        raise RuntimeError("compilation failed:\n" + "\n".join(msgs))
     tmp = LIB_PATH + ".tmp"
     link = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(link, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB_PATH)
+    os.replace(binding_tmp, BINDING_PATH)
     if verbose:
         for src in SOURCES:
-            with open(os.path.join(BUILD_DIR, src.replace(".cu", ".log"))) as f:
+            with open(os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".log")) as f:
                 sys.stdout.write(f.read())
     return LIB_PATH
 

@@ -1,0 +1,406 @@
+// Python binding of the operators around the expert forward: argument checks,
+// output allocation and the C-ABI call in one native function each, because
+// the smallest of these calls run for two to five microseconds and the same
+// steps through the interpreter take ten more.
+//
+// The C entry points are given by address (bind), so this module needs no
+// second copy of the library and no link to it.  A call returns its result, or
+// the library's non-zero status as an int for the caller to raise.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/cuda/EmptyTensor.h>
+#include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <exception>
+#include <string>
+#include <vector>
+
+#include "mxmoe.h"
+
+namespace {
+
+decltype(&mx_add_rmsnorm_quant) g_norm = nullptr;
+decltype(&mxfp8_linear_fused) g_linear = nullptr;
+decltype(&mxfp8_linear_fused_workspace_size) g_linear_ws = nullptr;
+decltype(&moe_balance_loss) g_balance = nullptr;
+decltype(&moe_balance_loss_workspace_size) g_balance_ws = nullptr;
+
+// More rows than this get payload rows a multiple of 128 bytes apart (below it
+// the product is bound by the weights' rows).
+constexpr int64_t kPadRows = 256;
+
+// A failed check: the Python exception's type and text.
+struct Bad {
+  PyObject* type;
+  std::string text;
+};
+[[noreturn]] void bad_value(const std::string& s) { throw Bad{PyExc_ValueError, s}; }
+[[noreturn]] void bad_type(const std::string& s) { throw Bad{PyExc_TypeError, s}; }
+
+std::string shape_text(at::IntArrayRef s) {
+  std::string t = "(";
+  for (size_t i = 0; i < s.size(); ++i) t += (i ? ", " : "") + std::to_string(s[i]);
+  return t + (s.size() == 1 ? ",)" : ")");
+}
+
+const at::Tensor& tensor(PyObject* o, const char* name) {
+  if (!THPVariable_Check(o)) bad_type(std::string(name) + " must be a torch.Tensor");
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_cuda())
+    bad_value(std::string(name) + " must be a CUDA tensor (the library has no CPU path)");
+  return t;
+}
+void dtype(const at::Tensor& t, const char* name, at::ScalarType a, at::ScalarType b) {
+  if (t.scalar_type() != a && t.scalar_type() != b)
+    bad_type(std::string(name) + ": expected " + toString(a) +
+             (a == b ? "" : std::string(" or ") + toString(b)) + ", got " +
+             toString(t.scalar_type()));
+}
+const at::Tensor& rows(PyObject* o, const char* name, at::ScalarType a, at::ScalarType b) {
+  const at::Tensor& t = tensor(o, name);
+  dtype(t, name, a, b);
+  if (!t.is_contiguous()) bad_value(std::string(name) + " must be contiguous");
+  return t;
+}
+const at::Tensor& rows(PyObject* o, const char* name, at::ScalarType a) { return rows(o, name, a, a); }
+
+void same_shape(const at::Tensor& t, const char* name, at::IntArrayRef want, const char* what) {
+  if (t.sizes() != want)
+    bad_value(std::string(name) + " is " + shape_text(t.sizes()) + ", " + what + " " +
+              shape_text(want));
+}
+void same_device(const at::Tensor& t, const char* name, const at::Tensor& x) {
+  if (t.device() != x.device()) bad_value(std::string(name) + " is on another device");
+}
+
+at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor& like) {
+  return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
+}
+int64_t pad128(int64_t n) { return (n + 127) / 128 * 128; }
+// Scales of [M, K] in the tensor-core layout.
+at::Tensor empty_scales(int64_t M, int64_t K, const at::Tensor& like) {
+  return empty({pad128(M), pad128(K) / 32}, at::kByte, like);
+}
+// An e4m3 payload to write; its rows are ld bytes apart.
+at::Tensor empty_payload(at::IntArrayRef shape, int64_t M, const at::Tensor& like, int64_t* ld) {
+  const int64_t K = shape.back();
+  *ld = K;
+  if (M <= kPadRows || K % 128 == 0 || shape.size() != 2) return empty(shape, at::kByte, like);
+  *ld = pad128(K);
+  at::Tensor wide = empty({M, *ld}, at::kByte, like);
+  wide.unsafeGetTensorImpl()->set_sizes_and_strides(shape, {*ld, 1});
+  return wide;
+}
+// The distance of a payload's rows: contiguous, or 2D with rows further apart.
+int64_t payload_rows(const at::Tensor& t, const char* name) {
+  const at::ScalarType s = t.scalar_type();
+  if (s != at::kByte && s != at::kFloat8_e4m3fn && s != at::kChar)
+    bad_type(std::string(name) + ": expected Byte, got " + toString(s));
+  if (t.is_contiguous()) return t.dim() ? t.sizes().back() : 0;
+  if (t.dim() == 2 && t.stride(1) == 1 && t.stride(0) >= t.size(1)) return t.stride(0);
+  bad_value(std::string(name) + " must be contiguous");
+}
+
+void set(PyObject* dict, const char* key, at::Tensor t) {
+  PyObject* o = THPVariable_Wrap(std::move(t));
+  if (!o || PyDict_SetItemString(dict, key, o) != 0) {
+    Py_XDECREF(o);
+    throw Bad{nullptr, ""};  // an exception is set
+  }
+  Py_DECREF(o);
+}
+
+struct Owned {
+  PyObject* o;
+  ~Owned() { Py_XDECREF(o); }
+  PyObject* release() {
+    PyObject* r = o;
+    o = nullptr;
+    return r;
+  }
+};
+
+bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+void* ptr(const at::Tensor& t) { return t.data_ptr(); }
+void* stream_of(const at::Tensor& t) {
+  return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
+}
+
+// x, weight, residual | None, eps, bf16_out, mma_scales, residual_out | None
+PyObject* norm(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0], "x");
+  dtype(x, "x", at::kBFloat16, at::kBFloat16);
+  const auto shape = x.sizes();
+  if (shape.empty()) bad_type("x must be a torch.Tensor of at least one dimension");
+  const int64_t H = shape.back(), M = H ? x.numel() / H : 0;
+  int64_t ldx = H;
+  if (shape.size() == 2 && (H <= 1 || x.stride(1) == 1)) {
+    if (M > 1) ldx = x.stride(0);
+    if (ldx < H) bad_value("x: overlapping rows");
+  } else if (!x.is_contiguous()) {
+    bad_value("x must be contiguous");
+  }
+  const at::Tensor& w = rows(a[1], "weight", at::kBFloat16, at::kFloat);
+  same_device(w, "weight", x);
+  if (w.dim() != 1 || w.size(0) != H)
+    bad_value("weight is " + shape_text(w.sizes()) + ", x has H = " + std::to_string(H));
+  const double eps = PyFloat_AsDouble(a[3]);
+  if (eps == -1.0 && PyErr_Occurred()) throw Bad{nullptr, ""};
+  const bool bf16_out = truth(a[4]), mma = truth(a[5]);
+  c10::cuda::CUDAGuard guard(x.device());
+  const void* res = nullptr;
+  at::Tensor out_res;
+  int res32 = 0;
+  if (a[2] != Py_None) {
+    const at::Tensor& r = rows(a[2], "residual", at::kBFloat16, at::kFloat);
+    same_device(r, "residual", x);
+    same_shape(r, "residual", shape, "x is");
+    res = ptr(r);
+    res32 = r.scalar_type() == at::kFloat;
+    if (a[6] == Py_None) {
+      out_res = empty(shape, r.scalar_type(), x);
+    } else {
+      out_res = rows(a[6], "residual_out", r.scalar_type());
+      same_device(out_res, "residual_out", x);
+      same_shape(out_res, "residual_out", shape, "x is");
+    }
+  } else if (a[6] != Py_None) {
+    bad_value("residual_out without a residual");
+  }
+  int64_t ldq = H;
+  at::Tensor q, s, y;
+  if (mma) {
+    q = empty_payload(shape, M, x, &ldq);
+    s = empty_scales(M, H, x);
+  } else {
+    q = empty(shape, at::kByte, x);
+    std::vector<int64_t> ss(shape.begin(), shape.end());
+    ss.back() = (H + 31) / 32;
+    s = empty(ss, at::kByte, x);
+  }
+  if (bf16_out) y = empty(shape, at::kBFloat16, x);
+  const int rc = g_norm((const uint16_t*)ptr(x), ldx, res, res32, res ? ptr(out_res) : nullptr, ptr(w),
+                        w.scalar_type() == at::kFloat, (float)eps, M, H,
+                        bf16_out ? (uint16_t*)ptr(y) : nullptr, (uint8_t*)ptr(q), ldq,
+                        (uint8_t*)ptr(s), mma, stream_of(x));
+  if (rc) return PyLong_FromLong(rc);
+  Owned d{PyDict_New()};
+  if (!d.o) return nullptr;
+  set(d.o, "q", std::move(q));
+  set(d.o, "s", std::move(s));
+  if (res) {
+    if (a[6] == Py_None) set(d.o, "residual", std::move(out_res));
+    else if (PyDict_SetItemString(d.o, "residual", a[6]) != 0) return nullptr;
+  }
+  if (bf16_out) set(d.o, "y", std::move(y));
+  return d.release();
+}
+
+// x | (q, s), wq, ws_mma, bias | None, act, residual | None, mx_out, out | None,
+// workspace | None
+PyObject* linear(PyObject* const* a) {
+  const at::Tensor& wq = tensor(a[1], "wq");
+  const int64_t ldw = payload_rows(wq, "wq");
+  if (wq.dim() != 2) bad_value("wq: expected 2 dims, got " + shape_text(wq.sizes()));
+  const int64_t N = wq.size(0), K = wq.size(1);
+  const at::Tensor& ws = rows(a[2], "ws_mma", at::kByte);
+  if (ws.numel() != pad128(N) * (pad128(K) / 32))
+    bad_value("ws_mma is not in the tensor-core layout of wq's scales");
+  const bool pair = PyTuple_Check(a[0]);
+  if (pair && PyTuple_GET_SIZE(a[0]) != 2) bad_value("x: a pair (q, s)");
+  const at::Tensor& x =
+      pair ? tensor(PyTuple_GET_ITEM(a[0], 0), "x[0]") : rows(a[0], "x", at::kBFloat16);
+  const auto xs = x.sizes();
+  if (xs.empty() || xs.back() != K)
+    bad_value("wq is " + shape_text(wq.sizes()) + ", x is " + shape_text(xs));
+  const int64_t M = K ? x.numel() / K : 0;
+  same_device(wq, "wq", x);
+  same_device(ws, "ws_mma", x);
+  const uint16_t* xp = nullptr;
+  const uint8_t *xq = nullptr, *xsp = nullptr;
+  int64_t ldx = 0;
+  if (pair) {
+    ldx = payload_rows(x, "x[0]");
+    const at::Tensor& sx = rows(PyTuple_GET_ITEM(a[0], 1), "x[1]", at::kByte);
+    same_device(sx, "x[1]", x);
+    if (sx.numel() != pad128(M) * (pad128(K) / 32))
+      bad_value("x's scales are not in the tensor-core layout");
+    xq = (const uint8_t*)ptr(x);
+    xsp = (const uint8_t*)ptr(sx);
+  } else {
+    xp = (const uint16_t*)ptr(x);
+  }
+  const void* bias = nullptr;
+  int bias32 = 0;
+  if (a[3] != Py_None) {
+    const at::Tensor& b = rows(a[3], "bias", at::kBFloat16, at::kFloat);
+    same_device(b, "bias", x);
+    if (b.dim() != 1 || b.size(0) != N)
+      bad_value("bias is " + shape_text(b.sizes()) + ", wq has N = " + std::to_string(N));
+    bias = ptr(b);
+    bias32 = b.scalar_type() == at::kFloat;
+  }
+  const long act = PyLong_AsLong(a[4]);
+  if (act == -1 && PyErr_Occurred()) throw Bad{nullptr, ""};
+  const bool mx = truth(a[6]);
+  std::vector<int64_t> shape(xs.begin(), xs.end());
+  shape.back() = N;
+  c10::cuda::CUDAGuard guard(x.device());
+  const uint16_t* res = nullptr;
+  if (a[5] != Py_None) {
+    if (mx) bad_value("an MXFP8 result takes no residual");
+    const at::Tensor& r = rows(a[5], "residual", at::kBFloat16);
+    same_device(r, "residual", x);
+    same_shape(r, "residual", shape, "the result");
+    res = (const uint16_t*)ptr(r);
+  }
+  at::Tensor out, os, work;
+  int64_t ldo = 0;
+  if (mx) {
+    if (a[7] != Py_None) bad_value("out holds a bf16 result");
+    out = empty_payload(shape, M, x, &ldo);
+    os = empty_scales(M, N, x);
+  } else if (a[7] == Py_None) {
+    out = empty(shape, at::kBFloat16, x);
+  } else {
+    out = rows(a[7], "out", at::kBFloat16);
+    same_device(out, "out", x);
+    same_shape(out, "out", shape, "the result");
+  }
+  void* wp = nullptr;
+  size_t wb = 0;
+  if (!pair) {
+    if (a[8] != Py_None) {
+      work = rows(a[8], "workspace", at::kByte);
+      same_device(work, "workspace", x);
+      wb = (size_t)work.numel();
+    } else if ((wb = g_linear_ws(M, N, K)) != 0) {
+      work = empty({(int64_t)wb}, at::kByte, x);
+    }
+    if (wb) wp = ptr(work);
+  }
+  const int rc = g_linear(xp, xq, ldx, xsp, (const uint8_t*)ptr(wq), ldw, (const uint8_t*)ptr(ws), M,
+                          N, K, bias, bias32, (int)act, res, mx ? nullptr : (uint16_t*)ptr(out),
+                          mx ? (uint8_t*)ptr(out) : nullptr, ldo, mx ? (uint8_t*)ptr(os) : nullptr,
+                          wp, wb, stream_of(x));
+  if (rc) return PyLong_FromLong(rc);
+  if (!mx) {
+    if (a[7] == Py_None) return THPVariable_Wrap(std::move(out));
+    Py_INCREF(a[7]);
+    return a[7];
+  }
+  Owned q{THPVariable_Wrap(std::move(out))}, s{THPVariable_Wrap(std::move(os))};
+  return q.o && s.o ? PyTuple_Pack(2, q.o, s.o) : nullptr;
+}
+
+// logits, topk_ids, mask | None, counts | None, coef, grad
+PyObject* balance(PyObject* const* a) {
+  const at::Tensor& z = tensor(a[0], "logits");
+  if (z.scalar_type() != at::kFloat || z.dim() != 2) bad_type("logits: expected fp32 [T, E]");
+  const int64_t T = z.size(0), E = z.size(1);
+  if (E > 1 && z.stride(1) != 1) bad_value("logits: a row must be contiguous");
+  const int64_t ldl = T > 1 ? z.stride(0) : E;
+  if (ldl < E) bad_value("logits: overlapping rows");
+  const at::Tensor& ids = rows(a[1], "topk_ids", at::kInt);
+  same_device(ids, "topk_ids", z);
+  if (ids.dim() != 2 || ids.size(0) != T) bad_value("logits and topk_ids disagree on T");
+  const uint8_t* mask = nullptr;
+  if (a[2] != Py_None) {
+    const at::Tensor& m = rows(a[2], "mask", at::kBool, at::kByte);
+    same_device(m, "mask", z);
+    same_shape(m, "mask", {T}, "logits have T:");
+    mask = (const uint8_t*)ptr(m);
+  }
+  const int64_t* given = nullptr;
+  if (a[3] != Py_None) {
+    const at::Tensor& c = rows(a[3], "counts", at::kLong);
+    same_device(c, "counts", z);
+    same_shape(c, "counts", {E}, "logits have E:");
+    given = (const int64_t*)ptr(c);
+  }
+  const double coef = PyFloat_AsDouble(a[4]);
+  if (coef == -1.0 && PyErr_Occurred()) throw Bad{nullptr, ""};
+  const bool grad = truth(a[5]);
+  c10::cuda::CUDAGuard guard(z.device());
+  const int64_t k = ids.size(1);
+  if (E > INT32_MAX || k > INT32_MAX) return PyLong_FromLong(MXMOE_ERR_SHAPE);
+  at::Tensor loss = empty({}, at::kFloat, z), counts = empty({E}, at::kLong, z), d, work;
+  const size_t wb = g_balance_ws(T, (int)E);
+  if (wb) work = empty({(int64_t)wb}, at::kByte, z);
+  if (grad) d = empty({T, E}, at::kFloat, z);
+  const int rc =
+      g_balance((const float*)ptr(z), ldl, (const int32_t*)ptr(ids), mask, given, T, (int)E, (int)k,
+                (float)coef, (float*)ptr(loss), (int64_t*)ptr(counts),
+                grad ? (float*)ptr(d) : nullptr, wb ? ptr(work) : nullptr, wb, stream_of(z));
+  if (rc) return PyLong_FromLong(rc);
+  Owned out{PyDict_New()};
+  if (!out.o) return nullptr;
+  set(out.o, "loss", std::move(loss));
+  set(out.o, "counts", std::move(counts));
+  if (grad) set(out.o, "dlogits", std::move(d));
+  return out.release();
+}
+
+// No C++ exception leaves an entry: failed checks and allocation errors become
+// Python exceptions.
+template <PyObject* (*kFn)(PyObject* const*), int kArgs>
+PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != kArgs || !g_norm) {
+    PyErr_SetString(PyExc_TypeError, "binding: wrong number of arguments, or not bound");
+    return nullptr;
+  }
+  try {
+    return kFn(args);
+  } catch (const Bad& b) {
+    if (b.type) PyErr_SetString(b.type, b.text.c_str());
+  } catch (const c10::OutOfMemoryError& e) {
+    PyObject* torch = PyImport_ImportModule("torch");
+    PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    PyErr_Clear();
+    PyErr_SetString(type ? type : PyExc_RuntimeError, e.what_without_backtrace());
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  void* p[5];
+  if (n != 5) {
+    PyErr_SetString(PyExc_TypeError, "bind: five addresses");
+    return nullptr;
+  }
+  for (int i = 0; i < 5; ++i) {
+    p[i] = PyLong_AsVoidPtr(a[i]);
+    if (!p[i]) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: a null address");
+      return nullptr;
+    }
+  }
+  g_norm = reinterpret_cast<decltype(g_norm)>(p[0]);
+  g_linear = reinterpret_cast<decltype(g_linear)>(p[1]);
+  g_linear_ws = reinterpret_cast<decltype(g_linear_ws)>(p[2]);
+  g_balance = reinterpret_cast<decltype(g_balance)>(p[3]);
+  g_balance_ws = reinterpret_cast<decltype(g_balance_ws)>(p[4]);
+  Py_RETURN_NONE;
+}
+
+#define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f))
+PyMethodDef g_methods[] = {
+    {"bind", FAST(bind), METH_FASTCALL, "addresses of the C entry points"},
+    {"norm", FAST((entry<norm, 7>)), METH_FASTCALL, "mx_add_rmsnorm_quant"},
+    {"linear", FAST((entry<linear, 9>)), METH_FASTCALL, "mxfp8_linear_fused"},
+    {"balance", FAST((entry<balance, 6>)), METH_FASTCALL, "moe_balance_loss"},
+    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods,
+                        nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__binding(void) { return PyModule_Create(&g_module); }
