@@ -124,7 +124,21 @@ struct Owned {
   }
 };
 
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o) {
+  const int b = PyObject_IsTrue(o);
+  if (b < 0) throw Bad{nullptr, ""};
+  return b != 0;
+}
+// Other Python threads run while a launch waits for room in the stream's queue.
+struct NoGil {
+  PyThreadState* state = PyEval_SaveThread();
+  ~NoGil() { PyEval_RestoreThread(state); }
+};
+template <class F, class... A>
+int call(F f, A... args) {
+  NoGil free;
+  return f(args...);
+}
 void* ptr(const at::Tensor& t) { return t.data_ptr(); }
 void* stream_of(const at::Tensor& t) {
   return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
@@ -183,10 +197,10 @@ PyObject* norm(PyObject* const* a) {
     s = empty(ss, at::kByte, x);
   }
   if (bf16_out) y = empty(shape, at::kBFloat16, x);
-  const int rc = g_norm((const uint16_t*)ptr(x), ldx, res, res32, res ? ptr(out_res) : nullptr, ptr(w),
-                        w.scalar_type() == at::kFloat, (float)eps, M, H,
-                        bf16_out ? (uint16_t*)ptr(y) : nullptr, (uint8_t*)ptr(q), ldq,
-                        (uint8_t*)ptr(s), mma, stream_of(x));
+  const int rc = call(g_norm, (const uint16_t*)ptr(x), ldx, res, res32,
+                      res ? ptr(out_res) : nullptr, ptr(w), w.scalar_type() == at::kFloat,
+                      (float)eps, M, H, bf16_out ? (uint16_t*)ptr(y) : nullptr, (uint8_t*)ptr(q),
+                      ldq, (uint8_t*)ptr(s), mma, stream_of(x));
   if (rc) return PyLong_FromLong(rc);
   Owned d{PyDict_New()};
   if (!d.o) return nullptr;
@@ -283,10 +297,10 @@ PyObject* linear(PyObject* const* a) {
     }
     if (wb) wp = ptr(work);
   }
-  const int rc = g_linear(xp, xq, ldx, xsp, (const uint8_t*)ptr(wq), ldw, (const uint8_t*)ptr(ws), M,
-                          N, K, bias, bias32, (int)act, res, mx ? nullptr : (uint16_t*)ptr(out),
-                          mx ? (uint8_t*)ptr(out) : nullptr, ldo, mx ? (uint8_t*)ptr(os) : nullptr,
-                          wp, wb, stream_of(x));
+  const int rc = call(g_linear, xp, xq, ldx, xsp, (const uint8_t*)ptr(wq), ldw,
+                      (const uint8_t*)ptr(ws), M, N, K, bias, bias32, (int)act, res,
+                      mx ? nullptr : (uint16_t*)ptr(out), mx ? (uint8_t*)ptr(out) : nullptr, ldo,
+                      mx ? (uint8_t*)ptr(os) : nullptr, wp, wb, stream_of(x));
   if (rc) return PyLong_FromLong(rc);
   if (!mx) {
     if (a[7] == Py_None) return THPVariable_Wrap(std::move(out));
@@ -333,9 +347,9 @@ PyObject* balance(PyObject* const* a) {
   if (wb) work = empty({(int64_t)wb}, at::kByte, z);
   if (grad) d = empty({T, E}, at::kFloat, z);
   const int rc =
-      g_balance((const float*)ptr(z), ldl, (const int32_t*)ptr(ids), mask, given, T, (int)E, (int)k,
-                (float)coef, (float*)ptr(loss), (int64_t*)ptr(counts),
-                grad ? (float*)ptr(d) : nullptr, wb ? ptr(work) : nullptr, wb, stream_of(z));
+      call(g_balance, (const float*)ptr(z), ldl, (const int32_t*)ptr(ids), mask, given, T, (int)E,
+           (int)k, (float)coef, (float*)ptr(loss), (int64_t*)ptr(counts),
+           grad ? (float*)ptr(d) : nullptr, wb ? ptr(work) : nullptr, wb, stream_of(z));
   if (rc) return PyLong_FromLong(rc);
   Owned out{PyDict_New()};
   if (!out.o) return nullptr;
