@@ -31,13 +31,12 @@ struct LinParams {
 
 // Activations.  silu(z) = z * s(z) with s(z) = 1 / (1 + e^-z), and since
 // (1 + tanh u) / 2 = s(2u), the tanh form of gelu is z * s(2u), u = sqrt(2 / pi) *
-// (z + 0.044715 z^3).  erfcf (CUDA's) keeps gelu's relative accuracy where
-// 1 + erf cancels.
+// (z + 0.044715 z^3).  The erf form is below.
 //
 // The hardware exp2 and reciprocal run at a quarter of a warp's instruction rate
 // each, so two elements share one reciprocal: with d = 1 + 2^x, 1 / d0 =
-// d1 / (d0 d1).  x is cut at 63 to keep d0 d1 finite: s below 2^-63 reads as
-// 2^-63, which no sum with anything of z's size can tell from zero.
+// d1 / (d0 d1), unless one of the thread's x is above 63 (d0 d1 would overflow) or NaN
+// (it would reach the other element): then each takes its own.
 constexpr float kLog2e = 1.4426950409f;
 constexpr float kGelu1 = -2.f * 0.7978845608f * kLog2e;  // -2u log2 e = z (kGelu1 + kGelu3 z^2)
 constexpr float kGelu3 = 0.044715f * kGelu1;
@@ -75,14 +74,68 @@ __device__ __forceinline__ F2 bf16x2_f2(uint32_t w) {
   return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// z * 1 / (1 + 2^x)
+// z / (1 + 2^x)
+template <bool kShared>
 __device__ __forceinline__ F2 gate(F2 z, F2 x) {
   float x0, x1, d0, d1;
   unpack(x, x0, x1);
-  const F2 d = add2(f2(ex2_approx(fminf(x0, 63.f)), ex2_approx(fminf(x1, 63.f))), f2(1.f, 1.f));
+  const F2 d = add2(f2(ex2_approx(x0), ex2_approx(x1)), f2(1.f, 1.f));
   unpack(d, d0, d1);
+  if (!kShared) return mul2(z, f2(rcp_approx(d0), rcp_approx(d1)));
   const float r = rcp_approx(d0 * d1);
   return mul2(z, mul2(f2(r, r), f2(d1, d0)));
+}
+template <bool kShared, int N>
+__device__ __forceinline__ void silu_all(F2 (&v)[N]) {
+  const F2 k = f2(-kLog2e, -kLog2e);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = gate<kShared>(v[i], mul2(v[i], k));
+}
+template <bool kShared, int N>
+__device__ __forceinline__ void gelu_tanh_all(F2 (&v)[N]) {
+  const F2 k1 = f2(kGelu1, kGelu1), k3 = f2(kGelu3, kGelu3);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    v[i] = gate<kShared>(v[i], mul2(v[i], fma2(k3, mul2(v[i], v[i]), k1)));
+}
+// The smallest value, NaN if there is one.
+template <int N>
+__device__ __forceinline__ float min_nan(const F2 (&v)[N]) {
+  float m = INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float a, b;
+    unpack(v[i], a, b);
+    asm("min.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(a), "f"(b));
+  }
+  return m;
+}
+
+// z Phi(z).  With t = |z|: Phi(-t) = e^(-t^2 / 2) g(t), g(t) = erfcx(t / sqrt 2) / 2,
+// which falls smoothly from 1/2 like 1 / t, so a polynomial in s = 1 / (1 + 0.3 t)
+// takes it: degree 6, fitted here for the smallest relative error over 0 <= t <=
+// 14, 2^-19; with the rounding of the exponent 2^-18.6 for t < 4 and 2^-16.6 down to
+// 2^-126, where e^.. ends.  The relative accuracy of the tail, lost in 1 + erf, stays.
+__device__ __forceinline__ F2 gelu(F2 z) {
+  constexpr float p[7] = {-7.994919724e-5f, 0.1212771162f, 0.1066898778f, 0.1648099379f,
+                          -0.0487187691f,   0.2406335771f, -0.08461260796f};
+  float z0, z1, d0, d1, h0, h1, c0, c1;
+  unpack(z, z0, z1);
+  // (past 16 e^.. is 0; a NaN comes back with the factor z)
+  const F2 t = f2(fminf(fabsf(z0), 16.f), fminf(fabsf(z1), 16.f));
+  const F2 one = f2(1.f, 1.f);
+  unpack(fma2(t, f2(0.3f, 0.3f), one), d0, d1);
+  const float r = rcp_approx(d0 * d1);
+  const F2 s = mul2(f2(r, r), f2(d1, d0));
+  F2 g = f2(p[6], p[6]);
+#pragma unroll
+  for (int i = 5; i >= 0; --i) g = fma2(g, s, f2(p[i], p[i]));
+  float x0, x1;
+  unpack(mul2(t, mul2(t, f2(-0.5f * kLog2e, -0.5f * kLog2e))), x0, x1);
+  const F2 h = mul2(f2(ex2_approx(x0), ex2_approx(x1)), g);
+  unpack(h, h0, h1);
+  unpack(fma2(h, f2(-1.f, -1.f), one), c0, c1);
+  return mul2(z, f2(z0 < 0.f ? h0 : c0, z1 < 0.f ? h1 : c1));
 }
 
 // One switch for a thread's 2 N values (act is uniform).
@@ -98,28 +151,21 @@ __device__ __forceinline__ void activate_all(int act, F2 (&v)[N]) {
       }
       break;
     case ACT_GELU:
-#pragma unroll 1
-      for (int i = 0; i < N; ++i) {
-        float a, b;
-        unpack(v[0], a, b);
-        const F2 g = f2(0.5f * a * erfcf(a * -0.70710678f), 0.5f * b * erfcf(b * -0.70710678f));
 #pragma unroll
-        for (int j = 0; j + 1 < N; ++j) v[j] = v[j + 1];  // the values rotate: one copy of the code
-        v[N - 1] = g;
-      }
+      for (int i = 0; i < N; ++i) v[i] = gelu(v[i]);
       break;
-    case ACT_GELU_TANH: {
-      const F2 k1 = f2(kGelu1, kGelu1), k3 = f2(kGelu3, kGelu3);
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = gate(v[i], mul2(v[i], fma2(k3, mul2(v[i], v[i]), k1)));
+    // x <= 63 from these z on.  (Each thread decides for its values, which are one
+    // row's: with the warp's vote a row's bits would depend on its neighbours.)
+    case ACT_GELU_TANH:
+      if (min_nan(v) >= -7.5f) gelu_tanh_all<true>(v);
+      else gelu_tanh_all<false>(v);
+      __syncwarp();
       break;
-    }
-    case ACT_SILU: {
-      const F2 k = f2(-kLog2e, -kLog2e);
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = gate(v[i], mul2(v[i], k));
+    case ACT_SILU:
+      if (min_nan(v) >= -43.f) silu_all<true>(v);
+      else silu_all<false>(v);
+      __syncwarp();
       break;
-    }
     default: break;
   }
 }

@@ -506,3 +506,17 @@ def test_operators_in_a_graph(mm):
         for a, b in zip(got, want):
             assert torch.equal(a, b)
     assert mm.device_status() == 0
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M", [40, 600])
+def test_linear_activation_tails(mm, M, act):
+    """The activations by themselves (the bias alone, from -16 to 16): nothing but the
+    activation's error and the bf16 rounding is left.  Results below 2^-100, where the
+    exponentials end, aside.  40 and 600 rows: the split and the pair kernel."""
+    z = np.arange(-256, 256) / 16.0
+    b = torch.from_numpy(z).to(DEV, torch.float32)
+    lin = mm.MXFP8FusedLinear.from_bf16(torch.zeros(512, 64, device=DEV).bfloat16(), bias=b, act=act)
+    got = f64(lin(torch.zeros(M, 64, device=DEV).bfloat16()))
+    want = block.activation(act, z)
+    assert np.all(np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(want) + 2.0 ** -100)
