@@ -17,16 +17,20 @@
 //      over a cluster's CTAs through distributed shared memory; one partial
 //      histogram per cluster (at most 18) goes to the workspace.
 //   2. balance_rows_kernel: every CTA adds the partial histograms into f (CTA 0
-//      writes the counts), then a warp per token; each CTA leaves the sum of
-//      its tokens' s_t, and the last CTA to finish adds those in CTA order, so
-//      the loss does not depend on the order in which the CTAs run.
+//      writes the counts), then a warp takes 1 to 32
+//      tokens at a time (8 experts a lane); each CTA leaves the sum of its
+//      tokens' s_t, and the last CTA to finish adds those in CTA order, so the
+//      loss does not depend on the order in which the CTAs run.
 // Up to 1024 tokens one cluster does both (balance_small_kernel): one launch,
 // no workspace.
 //
 // A logit of -inf has p = 0; a row of -inf only has p = 0 throughout.  NaN
 // (or +inf) in a row that is not masked reaches the loss and that row.
 //
-// Roofline: HBM-bound for many tokens (4 E bytes read, 4 E written per token).
+// Bound by HBM for many tokens (4 E bytes read, 4 E written per token): 65536 x
+// 256, k = 8, takes 33.0 us, 4.1 TB/s, of which the count kernel, the second launch, the
+// partial histograms and the last CTA's sum are 14 us whatever T (with nothing in the row
+// loop); 16384 x 128 takes 13.3 us, 64 x 8 (one launch) 4.5 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -40,7 +44,7 @@ constexpr int kErrDeviceCheck = 8;  // MXMOE_ERR_DEVICE_CHECK
 constexpr int kMaxE = 1024;
 constexpr int kCluster = 8;
 constexpr int kCountThreads = 512;
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 512;
 constexpr int kSmallThreads = 512;
 constexpr int64_t kSmallTokens = 1024;
 
@@ -135,150 +139,173 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
   cluster_sync();  // no CTA leaves while another may still read its shared memory
 }
 
-// Where a lane keeps expert i of its EPL: lane + 32 i, or with kGroup (E a
-// multiple of 4) groups of four, 4 lane + i % 4 + 128 (i / 4).  The place
-// depends on E alone and v4 (16-byte rows) only on how it is read, so the sums
-// and their bits do not depend on a tensor's alignment.
-template <bool kGroup>
-__device__ __forceinline__ int expert_at(int lane, int i) {
-  return kGroup ? 4 * lane + (i & 3) + 128 * (i >> 2) : lane + 32 * i;
+// A token takes G lanes of a warp (32 / G tokens side by side), EPL experts each: E
+// <= G EPL.  Where lane l of them keeps expert i: l + G i, or with kQuad (E a multiple
+// of 4) groups of four, 4 l + i % 4 + 4 G (i / 4).  The place depends on E alone and
+// v4 (16-byte rows) only on how it is read, so the sums and their bits do not depend
+// on a tensor's alignment.
+template <int G, bool kQuad>
+__device__ __forceinline__ int expert_at(int l, int i) {
+  return kQuad ? 4 * l + (i & 3) + 4 * G * (i >> 2) : l + G * i;
 }
-template <int EPL, bool kGroup>
-__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int lane, bool v4,
+template <int G, int EPL, bool kQuad>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int l, bool v4,
                                          float (&v)[EPL]) {
-  if (kGroup && v4) {
+  if (kQuad && v4) {
 #pragma unroll
     for (int i = 0; i < EPL; i += 4) {
+      const int e = expert_at<G, true>(l, i);
       float4 u = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (expert_at<true>(lane, i) < E)
-        u = __ldcs(reinterpret_cast<const float4*>(row + expert_at<true>(lane, i)));
+      if (e < E) u = __ldcs(reinterpret_cast<const float4*>(row + e));
       v[i] = u.x; v[i + 1] = u.y; v[i + 2] = u.z; v[i + 3] = u.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      v[i] = expert_at<kGroup>(lane, i) < E ? __ldcs(row + expert_at<kGroup>(lane, i)) : -INFINITY;
+    for (int i = 0; i < EPL; ++i) {
+      const int e = expert_at<G, kQuad>(l, i);
+      v[i] = e < E ? __ldcs(row + e) : -INFINITY;
+    }
   }
 }
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int off = G / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
 
-// The warp's walk over tokens t, t + step, ... < T.  c: the counts (f times their
-// sum) of the lane's experts.
-// The next token's logits are loaded before this one's arithmetic, the first
-// ones by start().  sum() is the tokens' sum of s_t (times the counts' sum), the same on every lane: two
-// fp32 words, the second the first one's rounding errors.
-template <int EPL, bool kGroup>
+// A warp's walk over tokens: those of t, t + step, ... < T (t: the lane's own, the
+// first of them the same distance from the warp's first).  c: the counts (f times
+// their sum) of the lane's experts.  The next tokens' logits are loaded before these
+// ones' arithmetic, the first ones by start().  A masked token, and one past T, is a
+// row of -inf: p = 0 throughout.  sum_to() gives the sum of s_t (times the counts' sum) over
+// the warp's tokens, kept in two fp32 words, the second the first one's rounding
+// errors.
+template <int G, int EPL, bool kQuad>
 struct RowWalk {
   static constexpr bool kAhead = EPL <= 16;  // (two rows of 32 would not fit in the registers)
   const float* logits;
   int64_t ldl;
   const uint8_t* mask;
   int64_t t, step, T;
-  int E, lane;
+  int E;
   bool v4;
+  int sub, l;  // the lane's token of the warp's, and its lane of the token's
   float v[EPL];
-  bool live;
   float sum_hi, sum_lo;
 
-  __device__ __forceinline__ void load(int64_t at, float (&x)[EPL], bool& l) {
-    l = !mask || mask[at] != 0;
-    if (l) load_row<EPL, kGroup>(logits + at * ldl, E, lane, v4, x);
+  __device__ __forceinline__ void load(int64_t at, float (&x)[EPL]) {
+    if (at < T && (!mask || mask[at] != 0)) {
+      load_row<G, EPL, kQuad>(logits + at * ldl, E, l, v4, x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) x[i] = -INFINITY;
+    }
   }
-  __device__ __forceinline__ void start() {
-    live = false;
+  // first: the warp's first token
+  __device__ __forceinline__ void start(int64_t first) {
+    const int lane = threadIdx.x & 31;
+    sub = lane / G;
+    l = lane % G;
+    t = first;
     sum_hi = sum_lo = 0.f;
-    if (kAhead && t < T) load(t, v, live);
+    if (kAhead) load(t + sub, v);
   }
   __device__ __forceinline__ void walk(const float (&c)[EPL], float scale, float* dlogits) {
     float w[EPL];
-    bool live_next = false;
     for (; t < T; t += step) {  // warp-uniform
-      if (!kAhead) load(t, v, live);
-      else if (t + step < T) load(t + step, w, live_next);
-      if (live) {
-        float m = v[0];
+      if (!kAhead) load(t + sub, v);
+      else load(t + step + sub, w);
+      float m = v[0];
 #pragma unroll
-        for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
+      for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        if (m == -INFINITY) m = 0.f;  // an empty row: every exp below is 0 (NaN stays NaN)
-        float z = 0.f, s = 0.f;
+      for (int off = G / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      if (m == -INFINITY) m = 0.f;  // an empty row: every exp below is 0 (NaN stays NaN)
+      float z = 0.f, s = 0.f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          v[i] = __expf(v[i] - m);
-          z += v[i];
-          s = fmaf(v[i], c[i], s);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-          z += __shfl_xor_sync(0xffffffffu, z, off);
-          s += __shfl_xor_sync(0xffffffffu, s, off);
-        }
-        const float iz = z == 0.f ? 0.f : 1.f / z;
-        s *= iz;
-        const float h = __fadd_rn(sum_hi, s);
-        sum_lo = __fadd_rn(sum_lo, two_sum_err(sum_hi, s, h));
-        sum_hi = h;
-        const float g = scale * iz;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) v[i] = g * v[i] * (c[i] - s);
-      } else {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) v[i] = 0.f;
+      for (int i = 0; i < EPL; ++i) {
+        v[i] = __expf(v[i] - m);
+        z += v[i];
+        s = fmaf(v[i], c[i], s);
       }
-      if (dlogits) {
-        float* out = dlogits + t * E;
-        if (kGroup && v4) {
+      z = group_sum<G>(z);
+      s = group_sum<G>(s);
+      const float iz = z == 0.f ? 0.f : 1.f / z;
+      s *= iz;
+      const float h = __fadd_rn(sum_hi, s);
+      sum_lo = __fadd_rn(sum_lo, two_sum_err(sum_hi, s, h));
+      sum_hi = h;
+      const float g = scale * iz;
 #pragma unroll
-          for (int i = 0; i < EPL; i += 4)
-            if (expert_at<true>(lane, i) < E)
-              __stcs(reinterpret_cast<float4*>(out + expert_at<true>(lane, i)),
+      for (int i = 0; i < EPL; ++i) v[i] = g * v[i] * (c[i] - s);
+      if (dlogits && t + sub < T) {
+        float* out = dlogits + (t + sub) * E;
+        if (kQuad && v4) {
+#pragma unroll
+          for (int i = 0; i < EPL; i += 4) {
+            const int e = expert_at<G, true>(l, i);
+            if (e < E)
+              __stcs(reinterpret_cast<float4*>(out + e),
                      make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+          }
         } else {
 #pragma unroll
-          for (int i = 0; i < EPL; ++i)
-            if (expert_at<kGroup>(lane, i) < E) __stcs(out + expert_at<kGroup>(lane, i), v[i]);
+          for (int i = 0; i < EPL; ++i) {
+            const int e = expert_at<G, kQuad>(l, i);
+            if (e < E) __stcs(out + e, v[i]);
+          }
         }
       }
       if (kAhead) {
-        live = live_next;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) v[i] = w[i];
       }
     }
   }
-  __device__ __forceinline__ double sum() const { return (double)sum_hi + (double)sum_lo; }
+  // (fp64 adds are slow here: one per warp, on lane 0)
+  __device__ __forceinline__ void sum_to(double* out) {
+#pragma unroll
+    for (int off = G; off < 32; off <<= 1) {
+      const float hi = __shfl_xor_sync(0xffffffffu, sum_hi, off);
+      const float lo = __shfl_xor_sync(0xffffffffu, sum_lo, off);
+      const float h = __fadd_rn(sum_hi, hi);
+      sum_lo = __fadd_rn(__fadd_rn(sum_lo, lo), two_sum_err(sum_hi, hi, h));
+      sum_hi = h;
+    }
+    if ((threadIdx.x & 31) == 0) *out = (double)sum_hi + (double)sum_lo;
+  }
 };
 
 // The counts the loss uses, c of the lane's experts in fp32 (given: loaded by
 // load_given before the own counts are known), and coef * E / (n sum c).  The
 // rows work on c instead of f = c / sum c; this factor brings the sum back, so
 // no CTA divides E times and none waits for another's total.
-template <int EPL, bool kGroup>
-__device__ __forceinline__ void load_given(const int64_t* __restrict__ counts_in, int E, int lane,
+template <int G, int EPL, bool kQuad>
+__device__ __forceinline__ void load_given(const int64_t* __restrict__ counts_in, int E,
                                            float (&c)[EPL]) {
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = expert_at<kGroup>(lane, i);
+    const int e = expert_at<G, kQuad>((int)(threadIdx.x % G), i);
     c[i] = counts_in && e < E ? (float)__ldg(counts_in + e) : 0.f;
   }
 }
-template <int EPL, bool kGroup>
-__device__ __forceinline__ float loss_scale(const int* s_cnt, bool given, int E, int lane,
-                                            float coef, float (&c)[EPL]) {
+template <int G, int EPL, bool kQuad>
+__device__ __forceinline__ float loss_scale(const int* s_cnt, bool given, int E, float coef,
+                                            float (&c)[EPL]) {
   float total = 0.f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = expert_at<kGroup>(lane, i);
+    const int e = expert_at<G, kQuad>((int)(threadIdx.x % G), i);
     if (!given && e < E) c[i] = (float)s_cnt[e];
     total += c[i];
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  total = group_sum<G>(total);
   const float n = (float)s_cnt[E];
   return n > 0.f && total > 0.f ? coef * (float)E / n / total : 0.f;
 }
 
-template <int EPL, bool kGroup>
+template <int G, int EPL, bool kQuad>
 __global__ void __launch_bounds__(kRowThreads)
     balance_rows_kernel(const float* __restrict__ logits, int64_t ldl,
                         const uint8_t* __restrict__ mask, const int64_t* __restrict__ counts_in,
@@ -291,11 +318,13 @@ __global__ void __launch_bounds__(kRowThreads)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_launch_dependents();
   pdl_wait();
-  RowWalk<EPL, kGroup> rows = {logits, ldl, mask, (int64_t)blockIdx.x * (kRowThreads / 32) + warp,
-                               (int64_t)gridDim.x * (kRowThreads / 32), T, E, lane, row4};
-  rows.start();
+  constexpr int64_t kTokens = 32 / G;  // of a warp at a time
+  const int64_t first = ((int64_t)blockIdx.x * (kRowThreads / 32) + warp) * kTokens;
+  RowWalk<G, EPL, kQuad> rows = {
+      logits, ldl, mask, first, (int64_t)gridDim.x * (kRowThreads / 32) * kTokens, T, E, row4};
+  rows.start(first);
   float c[EPL];
-  load_given<EPL, kGroup>(counts_in, E, lane, c);
+  load_given<G, EPL, kQuad>(counts_in, E, c);
   const int* part = reinterpret_cast<const int*>(ws) + kOffPart;
   for (int e = threadIdx.x; e <= E; e += kRowThreads) {
     int sum = 0;
@@ -305,21 +334,24 @@ __global__ void __launch_bounds__(kRowThreads)
     if (blockIdx.x == 0 && e < E) counts[e] = sum;
   }
   __syncthreads();
-  const float scale = loss_scale<EPL, kGroup>(s_cnt, counts_in != nullptr, E, lane, coef, c);
+  const float scale = loss_scale<G, EPL, kQuad>(s_cnt, counts_in != nullptr, E, coef, c);
   rows.walk(c, scale, dlogits);
-  if (lane == 0) s_sum[warp] = rows.sum();
+  rows.sum_to(&s_sum[warp]);
   __syncthreads();
   double* sums = reinterpret_cast<double*>(ws + off_sums(E, clusters));
   if (threadIdx.x == 0) {
     double a = 0.0;
     for (int w = 0; w < kRowThreads / 32; ++w) a += s_sum[w];
     sums[blockIdx.x] = a;
-    __threadfence();
-    s_last = atomicAdd(&ws[0], 1u) == gridDim.x - 1;
+    uint32_t before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                 : "=r"(before)
+                 : "l"(&ws[0])
+                 : "memory");
+    s_last = before == gridDim.x - 1;
   }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
   if (warp == 0) {
     double a = 0.0;
     for (int b = lane; b < (int)gridDim.x; b += 32) a += __ldcg(&sums[b]);
@@ -331,7 +363,7 @@ __global__ void __launch_bounds__(kRowThreads)
 
 // Few tokens: one cluster counts, then walks the rows; the CTAs' histograms and
 // sums meet through distributed shared memory.
-template <int EPL, bool kGroup>
+template <int G, int EPL, bool kQuad>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads)
     balance_small_kernel(const float* __restrict__ logits, int64_t ldl,
                          const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
@@ -350,10 +382,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads
   __syncthreads();
   const int64_t per = (T + kCluster - 1) / kCluster;
   const int64_t t0 = min(T, rank * per), t1 = min(T, t0 + per);
-  RowWalk<EPL, kGroup> rows = {logits, ldl, mask, t0 + warp, kWarps, t1, E, lane, row4};
-  rows.start();
+  const int64_t first = t0 + warp * (32 / G);
+  RowWalk<G, EPL, kQuad> rows = {logits, ldl, mask, first, kWarps * (32 / G), t1, E, row4};
+  rows.start(first);
   float c[EPL];
-  load_given<EPL, kGroup>(counts_in, E, lane, c);
+  load_given<G, EPL, kQuad>(counts_in, E, c);
   count_tokens(ids, mask, t0, t1, E, k, v4, s_hist, &s_hist[E], status);
   __syncthreads();
   cluster_sync();
@@ -364,9 +397,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads
     if (rank == 0 && e < E) counts[e] = sum;
   }
   __syncthreads();
-  const float scale = loss_scale<EPL, kGroup>(s_cnt, counts_in != nullptr, E, lane, coef, c);
+  const float scale = loss_scale<G, EPL, kQuad>(s_cnt, counts_in != nullptr, E, coef, c);
   rows.walk(c, scale, dlogits);
-  if (lane == 0) s_sum[warp] = rows.sum();
+  rows.sum_to(&s_sum[warp]);
   __syncthreads();
   if (threadIdx.x == 0) {
     double a = 0.0;
@@ -383,9 +416,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads
   cluster_sync();
 }
 
-static int row_blocks(int64_t T) {
+// Lanes of a token: 8 experts each up to E = 256, all 32 lanes from there on.  (A warp
+// per token: 65536 x 16, 60 and 16384 x 128 took 24.5, 26.7 and 13.3 us, against 12.0, 15.3 and
+// 13.6.)
+static int lanes_of(int E) {
+  int g = 1;
+  while (g < 32 && 8 * g < E) g *= 2;
+  return g;
+}
+// Two CTAs of 512 threads per SM: half the tickets of four CTAs of 256 (the tickets and
+// the last CTA's sum take 4 us with those: 15.2 us at 16384 x 128, 13.3 with these).
+// Above 256 experts a thread's registers leave room for one.
+static int row_blocks(int64_t T, int E) {
   return (int)std::max<int64_t>(
-      1, std::min<int64_t>(ceil_div(T, kRowThreads / 32), 4 * (int64_t)num_sms()));
+      1, std::min<int64_t>(ceil_div(T * lanes_of(E), kRowThreads),
+                               (E > 256 ? 1 : 2) * (int64_t)num_sms()));
 }
 // Clusters of the count kernel: 512 tokens per CTA, at most one CTA per SM.
 static int count_clusters(int64_t T) {
@@ -409,21 +454,22 @@ struct Args {
   uint32_t* ws;
 };
 
-template <int EPL, bool kGroup>
-static cudaError_t launch(const Args& a, cudaStream_t stream) {
-  int* st = device_status_ptr();
-  if (a.T <= kSmallTokens)
-    return launch_pdl(balance_small_kernel<EPL, kGroup>, dim3(kCluster), dim3(kSmallThreads), 0,
-                      stream, a.logits, a.ldl, a.ids, a.mask, a.counts_in, a.T, a.E, a.k, a.v4,
-                      a.coef, a.loss, a.counts, a.dlogits, a.row4, st);
+template <int EPL, bool kQuad>
+static cudaError_t launch_small(const Args& a, cudaStream_t stream) {
+  return launch_pdl(balance_small_kernel<32, EPL, kQuad>, dim3(kCluster), dim3(kSmallThreads), 0,
+                    stream, a.logits, a.ldl, a.ids, a.mask, a.counts_in, a.T, a.E, a.k, a.v4,
+                    a.coef, a.loss, a.counts, a.dlogits, a.row4, device_status_ptr());
+}
+template <int G, int EPL, bool kQuad>
+static cudaError_t launch_large(const Args& a, cudaStream_t stream) {
   const int clusters = count_clusters(a.T);
   const cudaError_t err =
       launch_pdl(balance_count_kernel, dim3(clusters * kCluster), dim3(kCountThreads), 0, stream,
-                 a.ids, a.mask, a.T, a.E, a.k, a.v4, a.ws, st);
+                 a.ids, a.mask, a.T, a.E, a.k, a.v4, a.ws, device_status_ptr());
   if (err != cudaSuccess) return err;
-  return launch_pdl(balance_rows_kernel<EPL, kGroup>, dim3(row_blocks(a.T)), dim3(kRowThreads), 0,
-                    stream, a.logits, a.ldl, a.mask, a.counts_in, a.T, a.E, a.coef, a.loss,
-                    a.counts, a.dlogits, a.ws, clusters, a.row4);
+  return launch_pdl(balance_rows_kernel<G, EPL, kQuad>, dim3(row_blocks(a.T, a.E)),
+                    dim3(kRowThreads), 0, stream, a.logits, a.ldl, a.mask, a.counts_in, a.T, a.E,
+                    a.coef, a.loss, a.counts, a.dlogits, a.ws, clusters, a.row4);
 }
 
 }  // namespace balance
@@ -431,7 +477,7 @@ static cudaError_t launch(const Args& a, cudaStream_t stream) {
 size_t balance_workspace_bytes(int64_t T, int E) {
   using namespace balance;
   if (T <= kSmallTokens) return 0;
-  return (size_t)off_sums(E, count_clusters(T)) * 4 + (size_t)row_blocks(T) * sizeof(double);
+  return (size_t)off_sums(E, count_clusters(T)) * 4 + (size_t)row_blocks(T, E) * sizeof(double);
 }
 
 cudaError_t launch_balance_loss(const float* logits, int64_t ldl, const int32_t* ids,
@@ -444,19 +490,36 @@ cudaError_t launch_balance_loss(const float* logits, int64_t ldl, const int32_t*
                     (((uintptr_t)logits | (uintptr_t)dlogits) & 15u) == 0;
   const Args a = {logits, ldl,  ids,  mask, counts_in, T,       E, k,
                   v4,     row4, coef, loss, counts,    dlogits, ws};
-  const int epl = (E + 31) / 32;
-  if (E % 4 == 0 && E > 64) {
-    if (epl <= 4) return launch<4, true>(a, stream);
-    if (epl <= 8) return launch<8, true>(a, stream);
-    if (epl <= 16) return launch<16, true>(a, stream);
-    return launch<32, true>(a, stream);
+  const bool quad = E % 4 == 0;
+  if (T <= kSmallTokens) {
+    // one token per warp and as few experts per lane as there are: few rows wait for
+    // one row's instructions (64 x 8: 4.5 us, and 5.7 with a lane per token)
+    if (E <= 32) return launch_small<1, false>(a, stream);
+    if (E <= 64) return launch_small<2, false>(a, stream);
+    if (E <= 128) return quad ? launch_small<4, true>(a, stream) : launch_small<4, false>(a, stream);
+    if (E <= 256) return quad ? launch_small<8, true>(a, stream) : launch_small<8, false>(a, stream);
+    if (E <= 512)
+      return quad ? launch_small<16, true>(a, stream) : launch_small<16, false>(a, stream);
+    return quad ? launch_small<32, true>(a, stream) : launch_small<32, false>(a, stream);
   }
-  if (epl <= 1) return launch<1, false>(a, stream);
-  if (epl <= 2) return launch<2, false>(a, stream);
-  if (epl <= 4) return launch<4, false>(a, stream);
-  if (epl <= 8) return launch<8, false>(a, stream);
-  if (epl <= 16) return launch<16, false>(a, stream);
-  return launch<32, false>(a, stream);
+  if (E > 512)
+    return quad ? launch_large<32, 32, true>(a, stream) : launch_large<32, 32, false>(a, stream);
+  if (E > 256)
+    return quad ? launch_large<32, 16, true>(a, stream) : launch_large<32, 16, false>(a, stream);
+  switch (quad ? lanes_of(E) : -lanes_of(E)) {
+    case 1: return launch_large<1, 8, true>(a, stream);
+    case 2: return launch_large<2, 8, true>(a, stream);
+    case 4: return launch_large<4, 8, true>(a, stream);
+    case 8: return launch_large<8, 8, true>(a, stream);
+    case 16: return launch_large<16, 8, true>(a, stream);
+    case 32: return launch_large<32, 8, true>(a, stream);
+    case -1: return launch_large<1, 8, false>(a, stream);
+    case -2: return launch_large<2, 8, false>(a, stream);
+    case -4: return launch_large<4, 8, false>(a, stream);
+    case -8: return launch_large<8, 8, false>(a, stream);
+    case -16: return launch_large<16, 8, false>(a, stream);
+    default: return launch_large<32, 8, false>(a, stream);
+  }
 }
 
 }  // namespace mxmoe
