@@ -486,10 +486,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         for (int i = 0; i < 2; ++i) {
           const int slot = lane + 32 * i;  // piece grp + GRPS (slot / PC), column slot % PC
           const int col = n0 + PC * (grp + GRPS * (slot / PC)) + slot % PC;
+          float b = 0.f;  // past N too: a row's arithmetic must not depend on what was there
           if (col < n0 + BN && col < p.N)
-            s_bias[slot] = p.bias32 ? __ldg(static_cast<const float*>(p.bias) + col)
-                                    : bf16_bits_to_float(
-                                          __ldg(static_cast<const uint16_t*>(p.bias) + col));
+            b = p.bias32 ? __ldg(static_cast<const float*>(p.bias) + col)
+                         : bf16_bits_to_float(__ldg(static_cast<const uint16_t*>(p.bias) + col));
+          s_bias[slot] = b;
         }
         __syncwarp();
       }

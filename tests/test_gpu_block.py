@@ -520,3 +520,20 @@ def test_linear_activation_tails(mm, M, act):
     got = f64(lin(torch.zeros(M, 64, device=DEV).bfloat16()))
     want = block.activation(act, z)
     assert np.all(np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(want) + 2.0 ** -100)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_linear_ragged_block_does_not_see_the_call_before(mm, act):
+    """N % 32 == 16: the half block past N holds nothing of an earlier call's bias."""
+    x, w = randn(1, 2048, 256).bfloat16(), randn(2, 1040, 256, scale=0.02).bfloat16()
+    lin = mm.MXFP8FusedLinear.from_bf16(w, bias=randn(3, 1040), act=act)
+    wide = randn(4, 1056, 256, scale=0.02).bfloat16()
+    got = []
+    for level in (-1e4, 0.0, float("nan")):
+        before = mm.MXFP8FusedLinear.from_bf16(wide, bias=torch.full((1056,), level, device=DEV),
+                                               act=act)
+        before(x, mx_out=True)
+        got.append(lin(x, mx_out=True))
+    torch.cuda.synchronize()
+    for q, s in got[1:]:
+        assert torch.equal(q, got[0][0]) and torch.equal(s, got[0][1])
