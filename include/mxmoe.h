@@ -418,8 +418,9 @@ mxmoe_status mx_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void* re
  *
  *   x          bf16 [M, K], MX-quantized first (the rule of mx_quantize_3d);
  *              or NULL, and then
- *   xq, xs     e4m3 [M, K], rows ldxq bytes apart, and its scales in the MMA layout (mx_add_rmsnorm_quant
- *              with mma_layout, or out_q / out_s of another call)
+ *   xq, xs     e4m3 [M, K], rows ldxq bytes apart, and its scales in the MMA
+ *              layout (mx_add_rmsnorm_quant with mma_layout, or out_q / out_s of
+ *              another call)
  *   wq, ws     e4m3 [N, K], rows ldwq bytes apart, and its scales in the MMA
  *              layout (mx_scales_to_mma_layout(ws, 1, N, K))
  *   bias       NULL, or [N] bf16 / (bias_fp32 != 0) fp32

@@ -5,9 +5,8 @@ tcgen05 tensor cores), with W4A8 (MXFP4 expert weights) and W4A4 (MXFP4
 weights and expert inputs) variants, the dense MXFP8 / W4A4 linear (one
 group of the grouped GEMM) and the operators around the expert forward in a
 transformer block (RMS norm with MXFP8 output, fused MXFP8 product, load-balance
-loss); ``api`` and ``block_ops`` are
-its thin Python binding and ``workloads``
-the seeded synthetic inputs.  Importing ``api`` functions loads the library
+loss); ``api`` and ``block_ops`` are its thin Python binding and ``workloads`` the
+seeded synthetic inputs.  Importing ``api`` functions loads the library
 lazily and raises if it has not been built.
 """
 

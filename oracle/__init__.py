@@ -17,6 +17,8 @@ method defines it, with no blocking, fusion or reordering:
   finalize-routing combine and the whole layer.
 * ``oracle.linear`` -- the dense MXFP8 linear (per-token activation quant,
   block-scaled GEMM, bf16 out), any K % 16 == 0.
+* ``oracle.block`` -- residual + RMS norm, the activations, the fused product
+  and the router's load-balance loss with its gradient.
 
 Sources (cited per function):
 
