@@ -21,7 +21,7 @@
 //      tokens at a time (8 experts a lane); each CTA leaves the sum of its
 //      tokens' s_t, and the last CTA to finish adds those in CTA order, so the
 //      loss does not depend on the order in which the CTAs run.
-// Up to 1024 tokens one cluster does both (balance_small_kernel): one launch,
+// For few tokens one cluster does both (balance_small_kernel): one launch,
 // no workspace.
 //
 // A logit of -inf has p = 0; a row of -inf only has p = 0 throughout.  NaN
@@ -46,7 +46,11 @@ constexpr int kCluster = 8;
 constexpr int kCountThreads = 512;
 constexpr int kRowThreads = 512;
 constexpr int kSmallThreads = 512;
-constexpr int64_t kSmallTokens = 1024;
+
+// One cluster, one launch: while its 128 warps have few tokens and experts to walk.
+// (us, one cluster against two launches: 1024 x 128 9.2 / 8.9, 768 x 256 10.0 / 9.7, 256 x
+// 1024 15.4 / 15.5; 1024 x 1024 25.9 / 15.5.)
+static bool is_small(int64_t T, int E) { return T <= 1024 && T * E <= 196608; }
 
 // Workspace, in 4-byte words: the CTA ticket, pad, then for each cluster of
 // the count kernel its token count and histogram [E], then (8-byte aligned)
@@ -476,7 +480,7 @@ static cudaError_t launch_large(const Args& a, cudaStream_t stream) {
 
 size_t balance_workspace_bytes(int64_t T, int E) {
   using namespace balance;
-  if (T <= kSmallTokens) return 0;
+  if (is_small(T, E)) return 0;
   return (size_t)off_sums(E, count_clusters(T)) * 4 + (size_t)row_blocks(T, E) * sizeof(double);
 }
 
@@ -491,7 +495,7 @@ cudaError_t launch_balance_loss(const float* logits, int64_t ldl, const int32_t*
   const Args a = {logits, ldl,  ids,  mask, counts_in, T,       E, k,
                   v4,     row4, coef, loss, counts,    dlogits, ws};
   const bool quad = E % 4 == 0;
-  if (T <= kSmallTokens) {
+  if (is_small(T, E)) {
     // one token per warp and as few experts per lane as there are: few rows wait for
     // one row's instructions (64 x 8: 4.5 us, and 5.7 with a lane per token)
     if (E <= 32) return launch_small<1, false>(a, stream);

@@ -11,8 +11,8 @@
 // are the bytes of mx_quantize_3d(y) and the router, which reads y, and the
 // products, which read q, see the same rows.  The sum of squares is fp32.
 //
-// A group of warps per row, 16 elements (half an MX block) per thread and chunk,
-// one or two chunks per thread, all of a row's loads in flight before the first
+// A group of warps, or part of a warp, per row, 16 elements (half an MX block) per
+// thread and chunk, one or two chunks per thread, all of a row's loads in flight before the first
 // is used, the row held in registers between the sum and the output: x and the
 // residual are read once, every output written once.
 //
@@ -38,7 +38,7 @@ struct Params {
   const void* w;
   float eps;
   int64_t M;
-  int H, wpr;  // row length, warps per row
+  int H, tpr, wpr;  // row length, threads (8, 16 or whole warps) and warps per row
   uint16_t* y;
   uint8_t* q;
   int64_t ldq;
@@ -88,7 +88,7 @@ template <int CPT, int kRes>
 __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const Params p) {
   __shared__ float s_red[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tpr = 32 * p.wpr;  // threads per row
+  const int tpr = p.tpr;
   const int rl = threadIdx.x / tpr, t = threadIdx.x - rl * tpr;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + rl;
   const bool row_ok = row < p.M;
@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const Params p)
     for (int j = 0; j < kChunk; ++j) ss = fmaf(h[i].get(j), h[i].get(j), ss);
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  for (int off = 16; off > 0; off >>= 1)
+    if (off < tpr) ss += __shfl_xor_sync(0xffffffffu, ss, off);
   if (p.wpr > 1) {  // uniform over the grid
     if (lane == 0) s_red[warp] = ss;
     __syncthreads();
@@ -254,10 +255,12 @@ cudaError_t launch_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void*
   p.tiled = tiled;
   p.x32 = ((uintptr_t)x & 31u) == 0 && ldx % 16 == 0;
   const int nch = H / kChunk;
-  // One CTA per row (four rows of up to 512 elements): a row's warps then wait for
-  // no other row.  Two chunks per thread for many long rows, where fewer warps
-  // meet at the barrier, and for rows of 2048 on without a residual, where one
-  // chunk's loads are too few; measured (us, bf16 residual unless said otherwise):
+  // One CTA per row: a row's warps then wait for no other row.  A warp, half or
+  // quarter of one for rows of up to 512, 256 and 128 elements, 128 threads per CTA
+  // (16384 x 64 and x 256: 3.4 and 6.3 us; 7.6 and 9.1 with a warp per row).  Two
+  // chunks per thread for many long rows, where fewer warps meet at the barrier, and
+  // for rows of 2048 on without a residual, where one chunk's loads are too few;
+  // measured (us, bf16 residual unless said otherwise):
   //   2048 x 12288 32.5 against 42.4 with one chunk, 4096 x 7168 34.9 / 41.7, 8192 x 4304
   //   42.1 / 44.3; 16384 x 2048 without a residual 28.8 / 31.6, with one 37.5 / 37.8;
   //   16384 x 1152 29.1 / 26.3 (the other way); 1 x 12288 2.9 / 2.7; with an fp32
@@ -266,9 +269,10 @@ cudaError_t launch_add_rmsnorm_quant(const uint16_t* x, int64_t ldx, const void*
   const int longest = res32 ? 384 : res ? 256 : 127;  // chunks of a row that takes one each
   const int cpt = nch > 1024 || (many && nch > longest) ? 2 : 1;
   p.wpr = (int)ceil_div(nch, 32 * cpt);
-  const int rows = p.wpr == 1 ? 4 : 1;
+  p.tpr = p.wpr > 1 ? 32 * p.wpr : nch <= 8 ? 8 : nch <= 16 ? 16 : 32;
+  const int rows = p.wpr == 1 ? 128 / p.tpr : 1;
   const int64_t grid = ceil_div(M, rows);
-  const dim3 block(32 * p.wpr * rows);
+  const dim3 block(p.tpr * rows);
   const int kind = !res ? 0 : res32 ? 2 : 1;
   auto kern = cpt == 1 ? (kind == 0   ? add_rmsnorm_quant_kernel<1, 0>
                           : kind == 1 ? add_rmsnorm_quant_kernel<1, 1>

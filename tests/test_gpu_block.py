@@ -537,3 +537,18 @@ def test_linear_ragged_block_does_not_see_the_call_before(mm, act):
     torch.cuda.synchronize()
     for q, s in got[1:]:
         assert torch.equal(q, got[0][0]) and torch.equal(s, got[0][1])
+
+
+@pytest.mark.parametrize("M,H", [(1, 128), (37, 112), (37, 144), (35, 256), (9, 272), (5, 512)])
+@pytest.mark.parametrize("mma_scales", [False, True])
+def test_norm_several_rows_per_warp(mm, M, H, mma_scales):
+    x, res = (randn(M + H + i, M, H, scale=3).bfloat16() for i in range(2))
+    check_norm(mm, x, randn(H, H), None, mma_scales=mma_scales)
+    check_norm(mm, x, randn(H, H).bfloat16(), res.float(), mma_scales=mma_scales)
+
+
+@pytest.mark.parametrize("T,E,k", [(768, 256, 8), (769, 256, 8), (193, 1024, 3), (192, 1024, 3),
+                                   (1024, 192, 2), (1030, 7, 3), (3000, 33, 4), (2000, 600, 8)])
+def test_balance_kernel_choice_edges(mm, T, E, k):
+    z, ids, mask = balance_case(T + E, T, E, k, 0.2)
+    check_balance(mm, z, ids, mask)
