@@ -512,9 +512,12 @@ static Plan make_plan(int64_t M, int N, int K) {
       if ((int)ceil_div(KT, kper) != s) continue;  // an empty range
       const int64_t ctas = tiles * s;
       // clusters in one wave only (second waves of clusters start late: 200 rows,
-      // 4096 x 12288 in clusters of 7 took 52 us), and of sizes that pack: on 152 SMs
-      // 144 can hold clusters of 4 and 120 clusters of 8
-      if (s == 5 || s == 7 || (s > 1 && ctas > slots * (s > 4 ? 0.9 : s > 2 ? 0.95 : 1.0))) continue;
+      // 4096 x 12288 in clusters of 7 took 52 us), and of sizes that pack: of 152 SMs with
+      // one CTA each, clusters of 3, 4, 6 and 8 can hold 138, 144, 138 and 120
+      // (4096 rows, 64 x 12288 took 26.6 us in 16 clusters of 8, 14.2 in 32 of 4)
+      const double held = s <= 2 ? 1.0 : slots > sms ? (s > 4 ? 0.9 : 0.95)
+                                       : s == 8 ? 0.79 : s == 4 ? 0.95 : 0.91;
+      if (s == 5 || s == 7 || (s > 1 && ctas > slots * held)) continue;
       const double waves = (double)ceil_div(ctas, slots);
       const double shared = ctas > sms && nt <= 64 ? 1.35 : 1.0;
       const double t = 3.1 + (nt == 128 ? 0.6 : nt == 256 ? 1.0 : 0.0) + (s > 1 ? 1.4 : 0.0) +
