@@ -45,13 +45,17 @@ constexpr int P_SEG = 2;                    // k-slices per scale segment
 constexpr int P_SFS = 4;                    // scale segments staged in shared memory
 constexpr int P_SF_BYTES = 4 * P_SEG * 512; // per segment: A chunks, three 128-row blocks of B
 
+// One pipeline stage less than shared memory would hold: what is left is the L1
+// cache through which the residual's loads pass (32 lines per load; us, with 6 and 5
+// stages: 16384 x 4304 x 1152 with a residual 106 and 84, 8192 x 4096 x 4096 95.6 and
+// 91.9; without one 16384 x 1152 x 4304 55.0 and 55.9; 4 stages: 84, 95, 58).
 // What a tile width leaves room for: pipeline stages in shared memory, scale
 // segments in tensor memory beside the two accumulators, each slice 4 (A) +
 // BN / 32 (B) columns rounded up to 4.
 template <int BN>
 struct Pair {
   static constexpr int B_BYTES = BN / 2 * BK;
-  static constexpr int STAGES = BN == 224 ? 6 : BN == 192 ? 7 : 8;
+  static constexpr int STAGES = BN == 224 ? 5 : BN == 192 ? 6 : 7;
   static constexpr int SLICE_COLS = (4 + BN / 32 + 3) / 4 * 4;
   static constexpr int SEG_COLS = P_SEG * SLICE_COLS;
   static constexpr int SF_COL = 2 * BN;
